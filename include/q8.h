@@ -76,7 +76,8 @@ typedef enum q8_format {
 } q8_format;
 
 typedef enum q8_op {
-  Q8_OP_LINEAR = 0, Q8_OP_DECOMP = 1, Q8_OP_FP8 = 2, Q8_OP_STATIC = 3, Q8_OP_GROUPED = 4
+  Q8_OP_LINEAR = 0, Q8_OP_DECOMP = 1, Q8_OP_FP8 = 2, Q8_OP_STATIC = 3, Q8_OP_GROUPED = 4,
+  Q8_OP_FP8_BLOCK = 5
 } q8_op;
 
 /*
@@ -346,6 +347,134 @@ q8_status q8_linear_noalloc(const void* x, q8_dtype x_dtype, int64_t M, int64_t 
                             const int8_t* wq, const float* w_scale, const float* w_zp,
                             int64_t N, const float* bias, void* y, q8_dtype y_dtype,
                             int32_t* acc_out, void* stream);
+
+/*
+ * The paged 8-bit key/value cache
+ * -------------------------------
+ * Keys and values of a layer are held as OCP e4m3fn codes in pages of `page`
+ * tokens (32, 64 or 128), with one power-of-two scale per page, kv head and
+ * tensor, kept as an exponent byte b: a code c stands for e4m3(c) 2^(b - 127).
+ *   k_cache  uint8 [num_pages, Hkv, page, D]   keys, the features of a token together
+ *   v_cache  uint8 [num_pages, Hkv, D, page]   values, the tokens of a feature together
+ *   k_exp, v_exp  uint8 [num_pages, Hkv]       exponent bytes
+ * D is 64, 128 or 256.  A scale that is a power of two costs e4m3 no precision
+ * (its precision is relative), lets a page's older codes be re-expressed
+ * exactly when a larger value joins them (bar values that leave e4m3's range
+ * below), and is applied by exponent arithmetic.  A byte of 255 must not occur.
+ *
+ * A batch of S sequences over the cache:
+ *   q_start      int32 [S + 1]: tokens q_start[s] .. q_start[s+1]-1 of the
+ *                token arrays are sequence s's new tokens (n of them, may be 0)
+ *   kv_len       int32 [S]: its length with the new tokens; new token i has
+ *                position kv_len[s] - n + i
+ *   block_table  int32 [S, max_pages]: page of positions page * j ..
+ *                page * j + page - 1 of sequence s at [s, j]
+ * All three are device memory, read on the device only.  max_q and max_kv are
+ * the caller's bounds on n and kv_len (they size grids and splits: too small a
+ * bound costs time, not results).  q_start is clamped to [0, T], a decreasing
+ * pair counts as no tokens; positions before 0 or past max_pages * page do not
+ * exist; page numbers outside [0, num_pages) are skipped by the append and read
+ * as the nearest page by the attention.  Nothing outside the arrays is read or
+ * written whatever these arrays hold.
+ */
+
+/*
+ * q8_kv_append -- put new keys and values into the cache and rotate the new
+ * queries, in one launch.  For sequence s's token at position p:
+ *     rotation (cos, sin given; features 0 .. rot_dim-1 of each head, r = rot_dim / 2):
+ *       interleaved = 0: pairs (i, i + r);  1: pairs (2 i, 2 i + 1);  i < r
+ *       (a, b) -> (a cos[p,i] - b sin[p,i], b cos[p,i] + a sin[p,i])   (binary32, uncontracted)
+ *     keys are rotated, values are not; q_out receives the rotated queries
+ *     rounded to their type.
+ * Each (page, kv head, tensor) that receives tokens:
+ *     want = least b >= 0 with max |new values| <= 448 2^(b - 127)
+ *     b'   = want if no older token lies in the page (it is started anew), else max(b, want)
+ *     older codes c -> e4m3_rne(e4m3(c) 2^(b - b')), new codes e4m3_rne(x 2^(127 - b'))
+ * Slots at or past kv_len, and those of other pages, keep their bytes.  Two
+ * sequences must not append to the same page in one call.
+ * k, v: [T, Hkv, D] and q: [T, Hq, D] of `dtype` (F32, F16, BF16), tokens
+ * k_stride, v_stride, q_stride elements apart (slices of one fused projection,
+ * say; multiples of 16 bytes), heads and features dense.  q and q_out may both
+ * be NULL (then Hq is ignored); q_out: [T, Hq, D] dense, may be q if q is dense.
+ * cos, sin: float [positions, rot_dim / 2], or both NULL (no rotation);
+ * positions past the table use its last row.  rot_dim: a multiple of 16 up to D.
+ * No workspace.  T = 0: arguments are checked, nothing is enqueued.
+ */
+q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, q8_dtype dtype, int64_t T, int64_t Hq,
+                       int64_t Hkv, int64_t D, const float* cos, const float* sin,
+                       int64_t positions, int64_t rot_dim, int interleaved,
+                       const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                       int64_t S, int64_t max_pages, int64_t max_q, uint8_t* k_cache,
+                       uint8_t* k_exp, uint8_t* v_cache, uint8_t* v_exp, int64_t num_pages,
+                       int64_t page, void* q_out, void* stream);
+
+/*
+ * q8_attention_kv8 -- softmax attention of the new queries over the cache.
+ * Query token at position p, head h (reads kv head h / (Hq / Hkv)); keys j of
+ * its sequence with j < kv_len, j <= p if causal, j > p - window if window > 0:
+ *     w_j = softmax_j(scale q . k_j),   out = sum_j w_j v_j,   lse = log sum_j exp(scale q . k_j)
+ * A query that sees no key gets out = 0 and lse = -inf.  Codes of keys that no
+ * query sees may hold anything, NaN codes included, and pages that lie wholly
+ * there need not exist.  Scores and values are exact products of the codes with
+ * the 16-bit queries and with the softmax weights rounded to f16; all sums,
+ * the maximum and the output accumulator are binary32.
+ * q: [T, Hq, D] of `dtype` (F16 or BF16), tokens q_stride elements apart (a
+ * multiple of 8); out: [T, Hq, D] of dtype; lse: float [T, Hq] or NULL.  Rows of
+ * tokens that belong to no sequence are left alone.  Hq is a multiple of Hkv.
+ * workspace: q8_attention_workspace_bytes(...) with the same sizes (0 where the
+ * keys are not split over workgroups).
+ */
+q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, int64_t Hq,
+                           int64_t Hkv, int64_t D, const int32_t* q_start, const int32_t* kv_len,
+                           const int32_t* block_table, int64_t S, int64_t max_pages, int64_t max_q,
+                           int64_t max_kv, const uint8_t* k_cache, const uint8_t* k_exp,
+                           const uint8_t* v_cache, const uint8_t* v_exp, int64_t num_pages,
+                           int64_t page, float scale, int causal, int64_t window, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace q8_attention_kv8 needs at these sizes; 0 for invalid ones,
+ * which the call itself then rejects. */
+size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S,
+                                    int64_t max_q, int64_t max_kv, int64_t window);
+
+/*
+ * Block-scaled FP8 linear: e4m3 codes with one scale per token and 128
+ * features of X and one per 128 rows x 128 features of W, the granularity of
+ * block-quantized FP8 checkpoints.  G = ceil(K / 128); the last block of a
+ * dimension may be short.
+ *
+ * q8_quantize_weight_block (once per weight) and q8_quantize_act_block:
+ *     S = max(max |.| over the block / 448, 1e-8),  q = e4m3_rne(clamp(. / S, -448, 448))
+ * w: [N, K], wq: uint8 [N, K], w_scale: float [ceil(N / 128), G].
+ * x: [M, K], xq: uint8 [M, K], x_scale: float [G, M] (block-major).
+ * w, x of type F32, F16 or BF16.
+ */
+q8_status q8_quantize_weight_block(const void* w, q8_dtype w_dtype, int64_t N, int64_t K,
+                                   uint8_t* wq, float* w_scale, void* stream);
+q8_status q8_quantize_act_block(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, uint8_t* xq,
+                                float* x_scale, void* stream);
+
+/*
+ * q8_gemm_fp8_block -- the product on quantized operands:
+ *     y[m,n] = sum_j S_x[j,m] S_w[n / 128, j] (sum_{k in block j} e4m3(xq[m,k]) e4m3(wq[n,k]))  (+ bias[n])
+ * The inner sums run on the FP8 matrix instruction, the outer in binary32.
+ * bias: float [N] or NULL; y: [M, N] of y_dtype (F16 or BF16: the
+ * instruction's sums do not carry binary32 precision).  No workspace.
+ */
+q8_status q8_gemm_fp8_block(const uint8_t* xq, const float* x_scale, int64_t M, int64_t K,
+                            const uint8_t* wq, const float* w_scale, int64_t N, const float* bias,
+                            void* y, q8_dtype y_dtype, void* stream);
+
+/*
+ * q8_linear_fp8_block -- q8_quantize_act_block followed by q8_gemm_fp8_block.
+ * x: [M, K] of x_dtype (F32, F16, BF16); y of y_dtype (F16 or BF16).
+ * workspace: q8_workspace_bytes(Q8_OP_FP8_BLOCK, M, N, K).
+ */
+q8_status q8_linear_fp8_block(const void* x, q8_dtype x_dtype, int64_t M, int64_t K,
+                              const uint8_t* wq, const float* w_scale, int64_t N,
+                              const float* bias, void* y, q8_dtype y_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace the call `op` needs at this shape (0 if none); returns 0
  * for invalid shapes as well, which the call itself then rejects. */

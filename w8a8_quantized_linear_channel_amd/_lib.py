@@ -21,6 +21,7 @@ STATUS_NAMES = {
 Q8_F32, Q8_F16, Q8_BF16 = 0, 1, 2
 Q8_INT8_ASYM, Q8_INT8_SYM, Q8_FP8_E4M3 = 0, 1, 2
 Q8_OP_LINEAR, Q8_OP_DECOMP, Q8_OP_FP8, Q8_OP_STATIC, Q8_OP_GROUPED = 0, 1, 2, 3, 4
+Q8_OP_FP8_BLOCK = 5
 
 # every symbol include/q8.h declares, with (restype, argtypes)
 _P = ctypes.c_void_p
@@ -44,6 +45,15 @@ SIGNATURES = {
     "q8_quantize_weight_grouped": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P]),
     "q8_linear_grouped": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _INT, _P, _SZ, _P]),
     "q8_linear_noalloc": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _I64, _P, _P, _INT, _P, _P]),
+    "q8_kv_append": (_INT, [_P, _I64, _P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _INT,
+                            _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P]),
+    "q8_attention_kv8": (_INT, [_P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64,
+                                _P, _P, _P, _P, _I64, _I64, _F, _INT, _I64, _P, _P, _P, _SZ, _P]),
+    "q8_attention_workspace_bytes": (_SZ, [_I64] * 8),
+    "q8_quantize_weight_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
+    "q8_quantize_act_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
+    "q8_gemm_fp8_block": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _INT, _P]),
+    "q8_linear_fp8_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _I64, _P, _P, _INT, _P, _SZ, _P]),
     "q8_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64]),
     # include/q8_bench.h
     "q8_bench_mfma_loop": (_INT, [_INT, _I64, _I64, _P, _P]),

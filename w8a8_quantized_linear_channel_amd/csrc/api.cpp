@@ -15,6 +15,7 @@
 #include "q8_bench_kernels.hpp"
 #include "q8_group.hpp"
 #include "q8_kernels.hpp"
+#include "q8_kv.hpp"
 #include "q8_linear_impl.hpp"
 
 namespace {
@@ -22,6 +23,7 @@ namespace {
 constexpr int64_t kMaxK = 65536;          // keeps acc - Z*rowsum inside int32 (|.| <= 32512 K)
 constexpr int64_t kMaxRows = (1LL << 31) - 1;
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxTokens = 1LL << 30;       // of one batch over the cache, and of a window
 constexpr int64_t kMaxGroups = 1024;            // experts of one grouped call (the kernels' bound)
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
@@ -146,6 +148,65 @@ Fp8Ws fp8_ws(int64_t M, int64_t K) {
   w.total = c.off;
   return w;
 }
+
+// Block-scaled FP8: codes and the scales [ceil(K / 128), M].
+Fp8Ws fp8_block_ws(int64_t M, int64_t K) {
+  Carve c;
+  Fp8Ws w;
+  w.xq = c.take((size_t)M * K);
+  w.xs = c.take((size_t)M * ((K + q8::kScaleBlock - 1) / q8::kScaleBlock) * 4);
+  w.total = c.off;
+  return w;
+}
+
+// Sizes shared by the calls on the paged cache.
+q8_status check_kv(int64_t T, int64_t Hkv, int64_t D, int64_t S, int64_t max_pages, int64_t max_q, int64_t num_pages,
+                   int64_t page) {
+  if (T < 0 || T > kMaxTokens || S < 1 || S > 32768 || Hkv < 1 || Hkv > 1024 || max_q < 0 || max_q > kMaxRows)
+    return Q8_ERR_BAD_SHAPE;
+  if (D != 64 && D != 128 && D != 256) return Q8_ERR_BAD_SHAPE;
+  if (page != 32 && page != 64 && page != 128) return Q8_ERR_BAD_SHAPE;
+  if (num_pages < 1 || num_pages > kMaxRows || max_pages < 1 || max_pages > kMaxRows / page - 256)
+    return Q8_ERR_BAD_SHAPE;
+  return Q8_OK;
+}
+bool valid_heads(int64_t Hq, int64_t Hkv) { return Hq >= 1 && Hq <= 65536 && Hq % Hkv == 0; }
+
+q8::KvView kv_view(const uint8_t* k, const uint8_t* ke, const uint8_t* v, const uint8_t* ve, const int32_t* q_start,
+                   const int32_t* kv_len, const int32_t* table, int64_t T, int64_t Hkv, int64_t S, int64_t max_pages,
+                   int64_t num_pages, int64_t page) {
+  q8::KvView kv{};
+  kv.k = const_cast<uint8_t*>(k);
+  kv.ke = const_cast<uint8_t*>(ke);
+  kv.v = const_cast<uint8_t*>(v);
+  kv.ve = const_cast<uint8_t*>(ve);
+  kv.q_start = q_start;
+  kv.kv_len = kv_len;
+  kv.table = table;
+  kv.num_pages = (int)num_pages;
+  kv.kv_heads = (int)Hkv;
+  kv.seqs = (int)S;
+  kv.max_pages = (int)max_pages;
+  kv.page = (int)page;
+  kv.tokens = (int)T;
+  return kv;
+}
+
+// Splits' partial sums: float [splits, T, Hq, D] and their (maximum, sum) pairs.
+struct AttnWs { size_t part, ml, total; };
+AttnWs attn_ws(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q, int64_t max_kv, int64_t window) {
+  AttnWs w{0, 0, 0};
+  if (T == 0) return w;
+  const int64_t splits = q8::attn_splits(T, (int)Hq, (int)Hkv, (int)S, max_q, max_kv, (int)window);
+  if (splits <= 1) return w;
+  Carve c;
+  w.part = c.take((size_t)splits * T * Hq * D * 4);
+  w.ml = c.take((size_t)splits * T * Hq * 8);
+  w.total = c.off;
+  return w;
+}
+// max_q and max_kv as the kernels use them: at least 1, at most what can occur
+int64_t bound_of(int64_t given, int64_t most) { return given < 1 ? 1 : (given > most ? (most < 1 ? 1 : most) : given); }
 
 // ---- device check: gfx950 only, cached per device
 constexpr int kMaxDevices = 64;
@@ -282,6 +343,7 @@ size_t q8_workspace_bytes(q8_op op, int64_t M, int64_t N, int64_t K) {
     case Q8_OP_FP8: return fp8_ws(M, K).total;
     case Q8_OP_STATIC: return static_ws(M, K).total;
     case Q8_OP_GROUPED: return grouped_ws(M, K).total;
+    case Q8_OP_FP8_BLOCK: return fp8_block_ws(M, K).total;
   }
   return 0;
 }
@@ -588,6 +650,175 @@ q8_status q8_linear_grouped(const void* x, q8_dtype x_dtype, int64_t M, int64_t 
   if (M <= q8::kGroupGemvMaxM)
     return launched(q8::launch_gemv_group(xq, xs, gs, M, K, wq, w_scale, w_zp, group, N, bias, y, y_dtype, st));
   return launched(q8::launch_gemm_group(xq, xs, gs, M, K, wq, w_scale, w_zp, group, N, bias, y, y_dtype, st));
+}
+
+q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       const float* cos, const float* sin, int64_t positions, int64_t rot_dim, int interleaved,
+                       const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int64_t S,
+                       int64_t max_pages, int64_t max_q, uint8_t* k_cache, uint8_t* k_exp, uint8_t* v_cache,
+                       uint8_t* v_exp, int64_t num_pages, int64_t page, void* q_out, void* stream) {
+  if (!valid_dtype(dtype)) return Q8_ERR_BAD_DTYPE;
+  Q8_TRY(check_kv(T, Hkv, D, S, max_pages, max_q, num_pages, page));
+  if (!q_start || !kv_len || !block_table || !k_cache || !k_exp || !v_cache || !v_exp || (T > 0 && (!k || !v)))
+    return Q8_ERR_NULL_PTR;
+  const bool rotate = cos != nullptr || sin != nullptr;
+  if (rotate && (!cos || !sin)) return Q8_ERR_NULL_PTR;
+  const bool has_q = q != nullptr || q_out != nullptr;
+  if (T > 0 && has_q && (!q || !q_out)) return Q8_ERR_NULL_PTR;
+  if (has_q && (Hq < 1 || Hq > 65536)) return Q8_ERR_BAD_SHAPE;
+  if (rotate && (positions < 1 || positions > kMaxRows || rot_dim < 16 || rot_dim > D || rot_dim % 16 != 0))
+    return Q8_ERR_BAD_SHAPE;
+  const int64_t unit = dtype == Q8_F32 ? 4 : 8;      // elements in 16 bytes
+  auto bad_stride = [&](int64_t st, int64_t H) { return st < H * D || st % unit != 0; };
+  if (T > 1 && (bad_stride(k_stride, Hkv) || bad_stride(v_stride, Hkv) || (has_q && bad_stride(q_stride, Hq))))
+    return Q8_ERR_BAD_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos) || !aligned16(sin) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(q_out) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table))
+    return Q8_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {q, k, v, cos, sin, q_start, kv_len, block_table, k_cache, k_exp, v_cache, v_exp, q_out}));
+  if (T == 0) return Q8_OK;
+  q8::AppendArgs a{};
+  a.kv = kv_view(k_cache, k_exp, v_cache, v_exp, q_start, kv_len, block_table, T, Hkv, S, max_pages, num_pages, page);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.heads = has_q ? (int)Hq : 1;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = rotate ? (int)positions : 1;
+  a.rot = rotate ? (int)rot_dim : 0;
+  a.interleaved = interleaved != 0;
+  const int64_t mq = bound_of(max_q, T);
+  int64_t reach = (mq + page - 2) / page + 1;        // pages that mq tokens can lie in
+  reach = reach > max_pages ? max_pages : reach;
+  a.reach = (int)reach;
+  a.max_q = (int)mq;
+  return launched(q8::launch_kv_append(a, dtype, (int)D, st));
+}
+
+size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q,
+                                    int64_t max_kv, int64_t window) {
+  if (check_kv(T, Hkv, D, S, 1, max_q, 1, 32) != Q8_OK || !valid_heads(Hq, Hkv) || max_kv < 0 || max_kv > kMaxRows ||
+      window < 0)
+    return 0;
+  window = window > kMaxTokens ? 0 : window;
+  return attn_ws(T, Hq, Hkv, D, S, bound_of(max_q, T), bound_of(max_kv, kMaxRows), window).total;
+}
+
+q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv,
+                           int64_t D, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                           int64_t S, int64_t max_pages, int64_t max_q, int64_t max_kv, const uint8_t* k_cache,
+                           const uint8_t* k_exp, const uint8_t* v_cache, const uint8_t* v_exp, int64_t num_pages,
+                           int64_t page, float scale, int causal, int64_t window, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != Q8_F16 && dtype != Q8_BF16) return Q8_ERR_BAD_DTYPE;
+  Q8_TRY(check_kv(T, Hkv, D, S, max_pages, max_q, num_pages, page));
+  if (!valid_heads(Hq, Hkv) || max_kv < 0 || max_kv > kMaxRows) return Q8_ERR_BAD_SHAPE;
+  if (T > 1 && (q_stride < Hq * D || q_stride % 8 != 0)) return Q8_ERR_BAD_SHAPE;
+  if (!q_start || !kv_len || !block_table || !k_cache || !k_exp || !v_cache || !v_exp || (T > 0 && (!q || !out)))
+    return Q8_ERR_NULL_PTR;
+  if (!std::isfinite(scale) || window < 0) return Q8_ERR_BAD_ARG;
+  window = window > kMaxTokens ? 0 : window;           // wider than any sequence: no window
+  const int64_t mq = bound_of(max_q, T), mkv = bound_of(max_kv, kMaxRows);
+  const AttnWs ws = attn_ws(T, Hq, Hkv, D, S, mq, mkv, window);
+  if (ws.total > 0 && (!workspace || workspace_bytes < ws.total)) return Q8_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || (lse && !aligned4(lse)) ||
+      (ws.total > 0 && !aligned16(workspace)) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table))
+    return Q8_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {q, q_start, kv_len, block_table, k_cache, k_exp, v_cache, v_exp, out, lse,
+                         ws.total > 0 ? workspace : nullptr}));
+  if (T == 0) return Q8_OK;
+  q8::AttnArgs a{};
+  a.kv = kv_view(k_cache, k_exp, v_cache, v_exp, q_start, kv_len, block_table, T, Hkv, S, max_pages, num_pages, page);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.lse = lse;
+  a.heads = (int)Hq;
+  a.causal = causal != 0;
+  a.window = (int)window;
+  a.max_q = (int)mq;
+  a.max_kv = mkv;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (ws.total > 0) {
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.ml);
+  }
+  return launched(q8::launch_attention(a, dtype, (int)D, st));
+}
+
+q8_status q8_quantize_weight_block(const void* w, q8_dtype w_dtype, int64_t N, int64_t K, uint8_t* wq, float* w_scale,
+                                   void* stream) {
+  if (!valid_dtype(w_dtype)) return Q8_ERR_BAD_DTYPE;
+  Q8_TRY(check_mk(N, K));
+  if (N * K > kMaxRows) return Q8_ERR_BAD_SHAPE;
+  if (!w || !wq || !w_scale) return Q8_ERR_NULL_PTR;
+  if (!aligned16(w) || !aligned16(wq) || !aligned16(w_scale)) return Q8_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {w, wq, w_scale}));
+  return launched(q8::launch_quant_weight_block(w, w_dtype, N, K, wq, w_scale, st));
+}
+
+q8_status q8_quantize_act_block(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, uint8_t* xq, float* x_scale,
+                                void* stream) {
+  if (!valid_dtype(x_dtype)) return Q8_ERR_BAD_DTYPE;
+  Q8_TRY(check_mk(M, K, 0));
+  if (M * K > kMaxRows) return Q8_ERR_BAD_SHAPE;
+  if (M > 0 && (!x || !xq || !x_scale)) return Q8_ERR_NULL_PTR;
+  if (!aligned16(x) || !aligned16(xq) || !aligned16(x_scale)) return Q8_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {x, xq, x_scale}));
+  if (M == 0) return Q8_OK;
+  return launched(q8::launch_quant_act_block(x, x_dtype, M, K, xq, x_scale, st));
+}
+
+q8_status q8_gemm_fp8_block(const uint8_t* xq, const float* x_scale, int64_t M, int64_t K, const uint8_t* wq,
+                            const float* w_scale, int64_t N, const float* bias, void* y, q8_dtype y_dtype,
+                            void* stream) {
+  if (y_dtype != Q8_F16 && y_dtype != Q8_BF16) return Q8_ERR_BAD_DTYPE;
+  Q8_TRY(check_mnk(M, N, K));
+  if (!wq || !w_scale || (M > 0 && (!xq || !x_scale || !y))) return Q8_ERR_NULL_PTR;
+  if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(y) ||
+      (bias && !aligned16(bias)))
+    return Q8_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {xq, x_scale, wq, w_scale, bias, y}));
+  if (M == 0) return Q8_OK;
+  return launched(q8::launch_gemm_fp8_block(xq, x_scale, M, K, wq, w_scale, N, bias, y, y_dtype, st));
+}
+
+q8_status q8_linear_fp8_block(const void* x, q8_dtype x_dtype, int64_t M, int64_t K, const uint8_t* wq,
+                              const float* w_scale, int64_t N, const float* bias, void* y, q8_dtype y_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(x_dtype) || (y_dtype != Q8_F16 && y_dtype != Q8_BF16)) return Q8_ERR_BAD_DTYPE;
+  Q8_TRY(check_mnk(M, N, K));
+  if (!wq || !w_scale || (M > 0 && (!x || !y))) return Q8_ERR_NULL_PTR;
+  const Fp8Ws ws = fp8_block_ws(M, K);
+  if (ws.total > 0 && (!workspace || workspace_bytes < ws.total)) return Q8_ERR_WORKSPACE;
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(y) || (bias && !aligned16(bias)) ||
+      (ws.total > 0 && !aligned16(workspace)))
+    return Q8_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {x, wq, w_scale, bias, y, ws.total > 0 ? workspace : nullptr}));
+  if (M == 0) return Q8_OK;
+  char* base = static_cast<char*>(workspace);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(base + ws.xq);
+  float* xs = reinterpret_cast<float*>(base + ws.xs);
+  Q8_TRY(launched(q8::launch_quant_act_block(x, x_dtype, M, K, xq, xs, st)));
+  return launched(q8::launch_gemm_fp8_block(xq, xs, M, K, wq, w_scale, N, bias, y, y_dtype, st));
 }
 
 q8_status q8_bench_mfma_loop(q8_format fmt, int64_t iters, int64_t workgroups, int32_t* sink, void* stream) {
