@@ -88,43 +88,323 @@ __global__ __launch_bounds__(kThreads) void k_quant_weight_block(const void* __r
   if (threadIdx.x == 0) w_scale[blockIdx.x] = s;
 }
 
-// One wave per 16 x 16 outputs, straight from memory.
-template <int YDT>
-__global__ __launch_bounds__(kThreads) void k_gemm_block(const uint8_t* __restrict__ xq, const float* __restrict__ x_scale,
+// ---------------------------------------------------------------- tiles
+// Y tiles of BM x BN by WM x WN waves, each FM x FN fragments of 32 x 32
+// (v_mfma_f32_32x32x64_f8f6f4, weights first: fragment (i, j) holds D[n][m],
+// lane l the 16 rows n of one column m).  One stage is one scale block, 128
+// bytes of K of every tile row, filled by LDS DMA NST - 1 stages ahead, with
+// the block's activation scales of the tile beside it.  A fragment's two MFMAs
+// of a block start from zero; its 16 sums are then multiplied by S_x S_w and
+// added to the accumulator while the next fragment's MFMAs run (two waves on
+// each SIMD).
+constexpr int kBK = kScaleBlock;
+constexpr int kXcds = 8;
+constexpr int kGroupM = 4;       // tile rows that share weight tiles in L2
+
+// 128-byte LDS rows, the 16-byte chunk c of row r at c ^ ((r >> 1) & 7): the 16
+// rows that a fragment read touches in one cycle cover all 64 banks once.
+__device__ __forceinline__ int swz_key(int row) { return (row >> 1) & 7; }
+
+// 64 x 4 bytes from per-lane addresses into 256 bytes of LDS (one float a lane)
+__device__ __forceinline__ void dma4(const void* gp, void* lds) {
+  const uint32_t m0 = (uint32_t)(uintptr_t)(lptr_t)lds;
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(m0), "v"(gp)
+               : "memory", "m0");
+#pragma clang diagnostic pop
+}
+
+template <int BM, int BN, int WM, int WN, int NST>
+struct Tile {
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  static constexpr int kStage = (BM + BN) * kBK;
+  static constexpr int kLoads = (BM + BN) / 8 / kWaves;    // 1 KB DMAs (8 rows) of a wave and stage
+  static constexpr int kScales = BM / 64;                  // 64-row DMAs of activation scales of a stage
+  static constexpr int kScaleBytes = BM * 4;
+  static constexpr int kPitch = TN * 4 + 16;               // epilogue staging of one 32-row slab
+  static constexpr int kLds = NST * (kStage + kScaleBytes);
+  static_assert((BM + BN) / 8 % kWaves == 0 && BM % 64 == 0 && kScales <= kWaves, "DMA split");
+  static_assert(kWaves * 32 * kPitch <= kLds, "the epilogue's staging fits");
+};
+
+template <int BM, int BN, int WM, int WN, int NST, int YDT>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
+    const uint8_t* __restrict__ xq, const float* __restrict__ x_scale, int M, int K, const uint8_t* __restrict__ wq,
+    const float* __restrict__ w_scale, int N, const float* __restrict__ bias, void* __restrict__ y) {
+  using TL = Tile<BM, BN, WM, WN, NST>;
+  constexpr int FM = TL::FM, FN = TL::FN;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[TL::kLds];
+  float* const ssc = (float*)(smem + NST * TL::kStage);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // XCD-contiguous renumbering of the tiles, kGroupM tile rows to a column group
+  const int ntm = (M + BM - 1) / BM, ntn = (N + BN - 1) / BN;
+  int m0, n0;
+  {
+    const int T = ntm * ntn, q = T / kXcds, r = T % kXcds;
+    const int x = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
+    const int b = x * q + (x < r ? x : r) + i;
+    const int per = kGroupM * ntn, g = b / per, first = g * kGroupM;
+    const int size = ntm - first < kGroupM ? ntm - first : kGroupM;
+    m0 = (first + (b - g * per) % size) * BM;
+    n0 = (b - g * per) / size * BN;
+  }
+  const int groups = (K + kBK - 1) / kBK, full = K / kBK;
+
+  // DMA: instruction d of this wave fills rows 8 (d kWaves + wave) .. + 7 of the stage (activation
+  // rows first); lane l lands at row l / 8, chunk l % 8, and fetches the chunk that belongs there.
+  // Rows past M or N repeat the last one and feed outputs that are not stored.
+  uint32_t off[TL::kLoads];
+#pragma unroll
+  for (int d = 0; d < TL::kLoads; ++d) {
+    const int r = (d * TL::kWaves + wave) * 8 + (lane >> 3);
+    int row = r < BM ? m0 + r : n0 + r - BM;
+    const int most = r < BM ? M - 1 : N - 1;
+    row = row < most ? row : most;
+    off[d] = (uint32_t)row * (uint32_t)K + (((lane & 7) ^ swz_key(r)) << 4);
+  }
+  const int srow = (wave % TL::kScales) * 64 + lane;
+  const float* const sbase = x_scale + (m0 + srow < M ? m0 + srow : M - 1);
+  auto dma = [&](int j) {
+    uint8_t* const st = smem + (j % NST) * TL::kStage;
+#pragma unroll
+    for (int d = 0; d < TL::kLoads; ++d) {
+      const int r8 = d * TL::kWaves + wave;
+      dma16((r8 * 8 < BM ? xq : wq) + (int64_t)j * kBK, off[d], st + r8 * 1024);
+    }
+    dma4(sbase + (int64_t)j * M, ssc + (j % NST) * BM + (wave % TL::kScales) * 64);
+  };
+  // a last block that K ends inside: through registers, zeros past K
+  auto tail = [&](int j) {
+    uint8_t* const st = smem + (j % NST) * TL::kStage;
+    for (int c = tid; c < (BM + BN) * 8; c += TL::kThreads) {
+      const int r = c >> 3, k = j * kBK + (c & 7) * 16;
+      int row = r < BM ? m0 + r : n0 + r - BM;
+      const int most = r < BM ? M - 1 : N - 1;
+      row = row < most ? row : most;
+      const uint8_t* p = (r < BM ? xq : wq) + (int64_t)row * K + k;
+      *(v4i*)(st + r * kBK + (((c & 7) ^ swz_key(r)) << 4)) = k < K ? *(const v4i*)p : v4i{0, 0, 0, 0};
+    }
+    if (tid < BM) ssc[(j % NST) * BM + tid] = x_scale[(int64_t)j * M + (m0 + tid < M ? m0 + tid : M - 1)];
+  };
+
+  v16f acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int f = 0; f < FN; ++f) acc[i][f] = v16f{};
+
+  const int lm = lane & 31, lh = lane >> 5;
+  // operand of row base + lane % 32, k-step ks: logical chunks 4 ks + 2 (lane / 32) + {0, 1}
+  const int lo = ((2 * lh) ^ swz_key(lm)) << 4;
+  auto frag = [&](const uint8_t* row, int ks) {
+    const v4i a = *(const v4i*)(row + (lo ^ (ks << 6))), b = *(const v4i*)(row + ((lo ^ 16) ^ (ks << 6)));
+    return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  };
+  const float* wsc[FN];
+#pragma unroll
+  for (int f = 0; f < FN; ++f) {
+    const int n = n0 + wn * TL::TN + 32 * f;
+    wsc[f] = w_scale + (int64_t)((n < N ? n : N - 1) / kScaleBlock) * groups;
+  }
+
+  auto compute = [&](int j) {
+    const uint8_t* const st = smem + (j % NST) * TL::kStage;
+    const uint8_t* const xa = st + (wm * TL::TM + lm) * kBK;
+    const uint8_t* const wb = st + (BM + wn * TL::TN + lm) * kBK;
+    float sw[FN];
+    v8i fb[FN][2];
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      sw[f] = wsc[f][j];
+      fb[f][0] = frag(wb + f * 32 * kBK, 0);
+      fb[f][1] = frag(wb + f * 32 * kBK, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const v8i a0 = frag(xa + i * 32 * kBK, 0), a1 = frag(xa + i * 32 * kBK, 1);
+      const float sx = ssc[(j % NST) * BM + wm * TL::TM + 32 * i + lm];
+      v16f part[FN];
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][0], a0, v16f{}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][1], a1, part[f], 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        const float s = sx * sw[f];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][f][r] = __builtin_fmaf(s, part[f][r], acc[i][f][r]);
+      }
+    }
+  };
+
+  // Stage j's loads are this wave's oldest; those of up to NST - 2 later stages may be in flight.
+  auto arrived = [&](int later) {
+    if (later >= 2 && NST > 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (TL::kLoads + 1)) : "memory");
+    else if (later >= 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(TL::kLoads + 1) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j)
+    if (j < full) dma(j);
+  for (int j = 0; j < full; ++j) {
+    const int later = full - 1 - j < NST - 2 ? full - 1 - j : NST - 2;
+    arrived(later);                                   // and every wave is past block j - 1
+    if (j + NST - 1 < full) dma(j + NST - 1);
+    compute(j);
+    __builtin_amdgcn_s_waitcnt(kLgkmcnt0);            // this wave's reads of the stage are done
+  }
+  if (groups > full) {
+    __syncthreads();
+    tail(full);
+    __syncthreads();
+    compute(full);
+  }
+
+  // epilogue: one 32-row slab of a wave at a time through padded LDS, back row-contiguous, 8 columns a lane
+  __syncthreads();
+  constexpr int kPitch = TL::kPitch, LPR = TL::TN / 8, RPI = 64 / LPR;
+  uint8_t* const stg = smem + wave * 32 * kPitch;
+  const int rc = lane % LPR, rr = lane / LPR;
+  const int n = n0 + wn * TL::TN + 8 * rc;
+  float b8[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b8[e] = bias && n + e < N ? bias[n + e] : 0.0f;
+  const bool vec = (N & 7) == 0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(v4f*)(stg + lm * kPitch + (32 * f + 8 * q + 4 * lh) * 4) =
+            v4f{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
+#pragma unroll
+    for (int t = 0; t < 32 / RPI; ++t) {
+      const int row = t * RPI + rr, m = m0 + wm * TL::TM + 32 * i + row;
+      const v4f a = *(const v4f*)(stg + row * kPitch + rc * 32), b = *(const v4f*)(stg + row * kPitch + rc * 32 + 16);
+      if (m >= M || n >= N) continue;
+      const float v[8] = {a[0] + b8[0], a[1] + b8[1], a[2] + b8[2], a[3] + b8[3],
+                          b[0] + b8[4], b[1] + b8[5], b[2] + b8[6], b[3] + b8[7]};
+      uint16_t* const o = (uint16_t*)y + (int64_t)m * N + n;
+      if (vec) {
+        const v4i p = {(int)pack2_out<YDT>(v[0], v[1]), (int)pack2_out<YDT>(v[2], v[3]), (int)pack2_out<YDT>(v[4], v[5]),
+                       (int)pack2_out<YDT>(v[6], v[7])};
+        __builtin_nontemporal_store(p, (v4i*)o);
+      } else {
+        for (int e = 0; e < 8 && n + e < N; ++e) store_out<YDT>(o, e, v[e]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few tokens
+// Decode-shaped: a workgroup owns 16 weight rows, its 4 waves take every
+// fourth block of K (v_mfma_f32_16x16x128_f8f6f4: one block an instruction),
+// up to kAhead blocks' weights requested ahead, straight into registers, and
+// join through LDS.  MF fragments of 16 tokens share a weight operand.
+constexpr int kAhead = 8;
+template <int MF, int YDT>
+__global__ __launch_bounds__(kThreads) void k_gemv_block(const uint8_t* __restrict__ xq, const float* __restrict__ x_scale,
                                                          int M, int K, const uint8_t* __restrict__ wq,
                                                          const float* __restrict__ w_scale, int N,
                                                          const float* __restrict__ bias, void* __restrict__ y) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kWaves = kThreads / 64;
+  __shared__ v4f part[kWaves][MF][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int across = (N + 63) / 64;
-  const int n0 = ((blockIdx.x % across) * (kThreads / 64) + wave) * 16, m0 = (blockIdx.x / across) * 16;
-  if (n0 >= N) return;
+  const int n0 = blockIdx.x * 16;
   const int groups = (K + kScaleBlock - 1) / kScaleBlock;
-  const int wr = n0 + lr < N ? n0 + lr : N - 1, xr = m0 + lr < M ? m0 + lr : M - 1;
-  const uint8_t* wp = wq + (int64_t)wr * K;
-  const uint8_t* xp = xq + (int64_t)xr * K;
-  v4f acc = {0, 0, 0, 0};
-  for (int j = 0; j < groups; ++j) {
-    v8i a, b;
+  const uint8_t* const wp = wq + (int64_t)(n0 + lr < N ? n0 + lr : N - 1) * K;
+  const float* const ws = w_scale + (int64_t)(n0 / kScaleBlock) * groups;
+  int xr[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) xr[f] = 16 * f + lr < M ? 16 * f + lr : M - 1;
+  v4f acc[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) acc[f] = v4f{0, 0, 0, 0};
+  // both halves of the lane's 32 bytes of block j; bytes past K are zeros
+  auto load = [&](const uint8_t* p, int j, v4i* o) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = j * kScaleBlock + 32 * lg + 16 * h;
-      const v4i u = k < K ? *(const v4i*)(wp + k) : v4i{0, 0, 0, 0};
-      const v4i w = k < K ? *(const v4i*)(xp + k) : v4i{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { a[4 * h + i] = u[i]; b[4 * h + i] = w[i]; }
+      const v4i v = *(const v4i*)(p + (k < K ? k : 0));
+      o[h] = k < K ? v : v4i{0, 0, 0, 0};
     }
-    const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-    const float sc = x_scale[(int64_t)j * M + xr] * w_scale[(int64_t)(n0 / kScaleBlock) * groups + j];
+  };
+  for (int j0 = wave; j0 < groups; j0 += kWaves * kAhead) {
+    v4i w[kAhead][2];
+    float s[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += sc * part[i];
-  }
-  if (m0 + lr >= M) return;
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + u * kWaves < groups ? j0 + u * kWaves : j0;
+      load(wp, j, w[u]);
+      s[u] = ws[j];
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + 4 * lg + i;
-    if (n < N) store_out<YDT>(y, (int64_t)(m0 + lr) * N + n, acc[i] + (bias ? bias[n] : 0.0f));
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + u * kWaves;
+      if (j < groups) {
+        const v8i a = {w[u][0][0], w[u][0][1], w[u][0][2], w[u][0][3], w[u][1][0], w[u][1][1], w[u][1][2], w[u][1][3]};
+#pragma unroll
+        for (int f = 0; f < MF; ++f) {
+          v4i x[2];
+          load(xq + (int64_t)xr[f] * K, j, x);
+          const v8i b = {x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
+          const float sc = s[u] * x_scale[(int64_t)j * M + xr[f]];
+          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[f][r] = __builtin_fmaf(sc, p[r], acc[f][r]);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) part[wave][f][lane] = acc[f];
+  __syncthreads();
+  for (int f = wave; f < MF; f += kWaves) {
+    const int m = 16 * f + lr;
+    if (m >= M) continue;
+    v4f t = part[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) t += part[w][f][lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = n0 + 4 * lg + r;
+      if (n < N) store_out<YDT>(y, (int64_t)m * N + n, t[r] + (bias ? bias[n] : 0.0f));
+    }
+  }
+}
+
+template <int YDT>
+hipError_t launch_product(const uint8_t* xq, const float* xs, int M, int K, const uint8_t* wq, const float* ws, int N,
+                          const float* bias, void* y, hipStream_t st) {
+  if (M <= 64) {
+    const unsigned grid = (unsigned)((N + 15) / 16);
+    if (M <= 16) k_gemv_block<1, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    else if (M <= 32) k_gemv_block<2, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    else k_gemv_block<4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    return hipGetLastError();
+  }
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192)
+    k_gemm_tiles<256, 256, 2, 4, 2, YDT><<<(unsigned)tiles(256, 256), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+  else if (tiles(128, 128) >= 192)
+    k_gemm_tiles<128, 128, 2, 4, 4, YDT><<<(unsigned)tiles(128, 128), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+  else
+    k_gemm_tiles<64, 64, 2, 2, 4, YDT><<<(unsigned)tiles(64, 64), 256, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -154,10 +434,8 @@ hipError_t launch_quant_act_block(const void* x, int dt, int64_t M, int64_t K, u
 
 hipError_t launch_gemm_fp8_block(const uint8_t* xq, const float* x_scale, int64_t M, int64_t K, const uint8_t* wq,
                                  const float* w_scale, int64_t N, const float* bias, void* y, int ydt, hipStream_t st) {
-  const unsigned grid = (unsigned)(((N + 63) / 64) * ((M + 15) / 16));
-  if (ydt == DT_F16) k_gemm_block<DT_F16><<<grid, kThreads, 0, st>>>(xq, x_scale, (int)M, (int)K, wq, w_scale, (int)N, bias, y);
-  else k_gemm_block<DT_BF16><<<grid, kThreads, 0, st>>>(xq, x_scale, (int)M, (int)K, wq, w_scale, (int)N, bias, y);
-  return hipGetLastError();
+  if (ydt == DT_F16) return launch_product<DT_F16>(xq, x_scale, (int)M, (int)K, wq, w_scale, (int)N, bias, y, st);
+  return launch_product<DT_BF16>(xq, x_scale, (int)M, (int)K, wq, w_scale, (int)N, bias, y, st);
 }
 
 }  // namespace q8
