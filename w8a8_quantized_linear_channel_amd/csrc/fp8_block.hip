@@ -105,16 +105,31 @@ constexpr int kGroupM = 4;       // tile rows that share weight tiles in L2
 // rows that a fragment read touches in one cycle cover all 64 banks once.
 __device__ __forceinline__ int swz_key(int row) { return (row >> 1) & 7; }
 
-// 64 x 4 bytes from per-lane addresses into 256 bytes of LDS (one float a lane)
-__device__ __forceinline__ void dma4(const void* gp, void* lds) {
-  const uint32_t m0 = (uint32_t)(uintptr_t)(lptr_t)lds;
+// LDS DMA through a buffer resource: 64 lanes x 16 (or 4) bytes from base + voff (per lane) + soff
+// into consecutive LDS; bytes past the resource's end arrive as zeros.  Inline asm for the reason
+// given at dma16 (q8_device.hpp); callers wait with vmcnt.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+__device__ __forceinline__ void dma16_buf(v4i rsrc, uint32_t voff, uint32_t soff, void* lds) {
+  const uint32_t m0 = (uint32_t)(uintptr_t)(lptr_t)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(m0), "v"(gp)
+               : "s"(m0), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
+}
+__device__ __forceinline__ void dma4_buf(v4i rsrc, uint32_t voff, uint32_t soff, void* lds) {
+  const uint32_t m0 = (uint32_t)(uintptr_t)(lptr_t)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(m0), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
+// Words of a raw byte buffer over [p, p + bytes)
+__device__ __forceinline__ v4i buffer_words(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+             __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
 template <int BM, int BN, int WM, int WN, int NST>
@@ -159,26 +174,24 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
 
   // DMA: instruction d of this wave fills rows 8 (d kWaves + wave) .. + 7 of the stage (activation
   // rows first); lane l lands at row l / 8, chunk l % 8, and fetches the chunk that belongs there.
-  // Rows past M or N repeat the last one and feed outputs that are not stored.
-  uint32_t off[TL::kLoads];
-#pragma unroll
-  for (int d = 0; d < TL::kLoads; ++d) {
-    const int r = (d * TL::kWaves + wave) * 8 + (lane >> 3);
-    int row = r < BM ? m0 + r : n0 + r - BM;
-    const int most = r < BM ? M - 1 : N - 1;
-    row = row < most ? row : most;
-    off[d] = (uint32_t)row * (uint32_t)K + (((lane & 7) ^ swz_key(r)) << 4);
-  }
-  const int srow = (wave % TL::kScales) * 64 + lane;
-  const float* const sbase = x_scale + (m0 + srow < M ? m0 + srow : M - 1);
-  auto dma = [&](int j) {
-    uint8_t* const st = smem + (j % NST) * TL::kStage;
+  // Rows past M or N read what follows (zeros past the arrays) and feed outputs that are not stored.
+  constexpr int kStep = TL::kWaves * 8;                      // rows from one DMA to the next
+  const int r0 = wave * 8 + (lane >> 3);
+  const uint32_t chunk = (uint32_t)((lane & 7) ^ swz_key(r0)) << 4;
+  const uint32_t offx = (uint32_t)(m0 + r0) * (uint32_t)K + chunk, offw = (uint32_t)(n0 + r0) * (uint32_t)K + chunk;
+  const uint32_t offs = (uint32_t)(m0 + (wave % TL::kScales) * 64 + lane) * 4u;
+  const v4i resx = buffer_words(xq, (uint32_t)M * (uint32_t)K), resw = buffer_words(wq, (uint32_t)N * (uint32_t)K);
+  const v4i ress = buffer_words(x_scale, (uint32_t)M * (uint32_t)groups * 4u);
+  auto dma = [&](int j, int slot) {
+    uint8_t* const st = smem + slot * TL::kStage + wave * 1024;
 #pragma unroll
     for (int d = 0; d < TL::kLoads; ++d) {
-      const int r8 = d * TL::kWaves + wave;
-      dma16((r8 * 8 < BM ? xq : wq) + (int64_t)j * kBK, off[d], st + r8 * 1024);
+      const bool w = d * kStep >= BM;
+      // the row step belongs to the per-lane offset: the range check takes the scalar one off the size
+      const uint32_t step = (uint32_t)(w ? d * kStep - BM : d * kStep) * (uint32_t)K;
+      dma16_buf(w ? resw : resx, (w ? offw : offx) + step, (uint32_t)j * kBK, st + d * TL::kWaves * 1024);
     }
-    dma4(sbase + (int64_t)j * M, ssc + (j % NST) * BM + (wave % TL::kScales) * 64);
+    dma4_buf(ress, offs, (uint32_t)j * (uint32_t)M * 4u, ssc + slot * BM + (wave % TL::kScales) * 64);
   };
   // a last block that K ends inside: through registers, zeros past K
   auto tail = [&](int j) {
@@ -214,62 +227,96 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     wsc[f] = w_scale + (int64_t)((n < N ? n : N - 1) / kScaleBlock) * groups;
   }
 
-  auto compute = [&](int j) {
-    const uint8_t* const st = smem + (j % NST) * TL::kStage;
-    const uint8_t* const xa = st + (wm * TL::TM + lm) * kBK;
-    const uint8_t* const wb = st + (BM + wn * TL::TN + lm) * kBK;
-    float sw[FN];
-    v8i fb[FN][2];
+  // The fragments of a block: the weights' (kept over the block) and one row fragment's at a time,
+  // whose LDS reads run behind the FMAs of the fragment before.
+  float sw[FN], swn[FN], sx;
+  v8i fb[FN][2], fa[2];
+  auto load_b = [&](int j) {
+    const uint8_t* const wb = smem + (j % NST) * TL::kStage + (BM + wn * TL::TN + lm) * kBK;
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
-      sw[f] = wsc[f][j];
       fb[f][0] = frag(wb + f * 32 * kBK, 0);
       fb[f][1] = frag(wb + f * 32 * kBK, 1);
     }
+  };
+  auto load_a = [&](int j, int i) {
+    const uint8_t* const xa = smem + (j % NST) * TL::kStage + (wm * TL::TM + lm + 32 * i) * kBK;
+    fa[0] = frag(xa, 0);
+    fa[1] = frag(xa, 1);
+  };
+  auto load_s = [&](int j) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f) swn[f] = wsc[f][j];
+  };
+  // Block j; `next` (uniform) runs once this wave has read all of it, between the last MFMAs and their FMAs.
+  auto block = [&](int j, auto&& next) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f) sw[f] = swn[f];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const v8i a0 = frag(xa + i * 32 * kBK, 0), a1 = frag(xa + i * 32 * kBK, 1);
-      const float sx = ssc[(j % NST) * BM + wm * TL::TM + 32 * i + lm];
+      sx = ssc[(j % NST) * BM + wm * TL::TM + 32 * i + lm];
       v16f part[FN];
 #pragma unroll
       for (int f = 0; f < FN; ++f)
-        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][0], a0, v16f{}, 0, 0, 0, 0, 0, 0);
+        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][0], fa[0], v16f{}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
       for (int f = 0; f < FN; ++f)
-        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][1], a1, part[f], 0, 0, 0, 0, 0, 0);
+        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][1], fa[1], part[f], 0, 0, 0, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 1 < FM) load_a(j, i + 1);
+      else next();
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int f = 0; f < FN; ++f) {
         const float s = sx * sw[f];
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][f][r] = __builtin_fmaf(s, part[f][r], acc[i][f][r]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // Stage j's loads are this wave's oldest; those of up to NST - 2 later stages may be in flight.
-  auto arrived = [&](int later) {
-    if (later >= 2 && NST > 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (TL::kLoads + 1)) : "memory");
-    else if (later >= 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(TL::kLoads + 1) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // All NST buffers are filled ahead, a buffer again as soon as every wave has read its block.  Past
+  // the last full block the DMA repeats it, into buffers nobody reads, so that the loop has no
+  // branch and the number of loads in flight is always the same.
+  auto arrived = [&] {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (TL::kLoads + 1)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  auto clamped = [&](int b) { return b < full ? b : full - 1; };
+  int j = 0;
+  if (full > 0) {
 #pragma unroll
-  for (int j = 0; j < NST - 1; ++j)
-    if (j < full) dma(j);
-  for (int j = 0; j < full; ++j) {
-    const int later = full - 1 - j < NST - 2 ? full - 1 - j : NST - 2;
-    arrived(later);                                   // and every wave is past block j - 1
-    if (j + NST - 1 < full) dma(j + NST - 1);
-    compute(j);
-    __builtin_amdgcn_s_waitcnt(kLgkmcnt0);            // this wave's reads of the stage are done
+    for (int b = 0; b < NST - 1; ++b) dma(clamped(b), b);
+    arrived();
+    dma(clamped(NST - 1), NST - 1);
+    load_b(0);
+    load_a(0, 0);
+    load_s(0);
+    for (; j + 1 < full; ++j)
+      block(j, [&] {
+        __builtin_amdgcn_s_waitcnt(kLgkmcnt0);          // this wave's reads of block j are done
+        arrived();
+        dma(clamped(j + NST), j % NST);
+        load_b(j + 1);
+        load_a(j + 1, 0);
+        load_s(j + 1);
+      });
   }
-  if (groups > full) {
-    __syncthreads();
-    tail(full);
-    __syncthreads();
-    compute(full);
+  for (; j < groups; ++j) {
+    if (j >= full) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      tail(j);
+      __syncthreads();
+      load_b(j);
+      load_a(j, 0);
+      load_s(j);
+    }
+    block(j, [] {});
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // repeated blocks still on their way
 
   // epilogue: one 32-row slab of a wave at a time through padded LDS, back row-contiguous, 8 columns a lane
   __syncthreads();
