@@ -4,6 +4,8 @@
 //     y[m,n] = sum_j S_x[j,m] S_w[n / 128, j] sum_{k in j} e4m3(xq[m,k]) e4m3(wq[n,k])  (+ b[n])
 // Each block's inner sum is one chain of MFMAs started at zero, multiplied by
 // its scale in fp32 and added to the fp32 accumulator.
+#include <type_traits>
+
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
 
@@ -89,14 +91,15 @@ __global__ __launch_bounds__(kThreads) void k_quant_weight_block(const void* __r
 }
 
 // ---------------------------------------------------------------- tiles
-// Y tiles of BM x BN by WM x WN waves, each FM x FN fragments of 32 x 32
-// (v_mfma_f32_32x32x64_f8f6f4, weights first: fragment (i, j) holds D[n][m],
-// lane l the 16 rows n of one column m).  One stage is one scale block, 128
-// bytes of K of every tile row, filled by LDS DMA NST - 1 stages ahead, with
-// the block's activation scales of the tile beside it.  A fragment's two MFMAs
-// of a block start from zero; its 16 sums are then multiplied by S_x S_w and
-// added to the accumulator while the next fragment's MFMAs run (two waves on
-// each SIMD).
+// Y tiles of BM x BN by WM x WN waves, each AF x BF fragments of 16 x 16
+// (v_mfma_f32_16x16x128_f8f6f4, weights first: a fragment holds D[n][m], lane l
+// four rows n of column m = l % 16).  One instruction is one scale block, so a
+// block's sums start from zero, are multiplied by S_x S_w and added to the
+// accumulator with no second instruction in between (the 32 x 32 x 64 shape
+// needs two, and four times the registers for the sums: 243 against 233 us at
+// 4096 x 4096 x 14336 in the kernel trace).
+// One stage is one block, 128 bytes of K of every tile row, filled by LDS DMA
+// with the block's activation scales of the tile beside it.
 constexpr int kBK = kScaleBlock;
 constexpr int kXcds = 8;
 constexpr int kGroupM = 4;       // tile rows that share weight tiles in L2
@@ -135,15 +138,15 @@ __device__ __forceinline__ v4i buffer_words(const void* p, uint32_t bytes) {
 template <int BM, int BN, int WM, int WN, int NST>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  static constexpr int TM = BM / WM, TN = BN / WN, AF = TM / 16, BF = TN / 16, H = AF / 2;
   static constexpr int kStage = (BM + BN) * kBK;
   static constexpr int kLoads = (BM + BN) / 8 / kWaves;    // 1 KB DMAs (8 rows) of a wave and stage
   static constexpr int kScales = BM / 64;                  // 64-row DMAs of activation scales of a stage
   static constexpr int kScaleBytes = BM * 4;
-  static constexpr int kPitch = TN * 4 + 16;               // epilogue staging of one 32-row slab
+  static constexpr int kPitch = TN * 4 + 16;               // epilogue staging of one 16-row slab
   static constexpr int kLds = NST * (kStage + kScaleBytes);
   static_assert((BM + BN) / 8 % kWaves == 0 && BM % 64 == 0 && kScales <= kWaves, "DMA split");
-  static_assert(kWaves * 32 * kPitch <= kLds, "the epilogue's staging fits");
+  static_assert(kWaves * 16 * kPitch <= kLds, "the epilogue's staging fits");
 };
 
 template <int BM, int BN, int WM, int WN, int NST, int YDT>
@@ -151,7 +154,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     const uint8_t* __restrict__ xq, const float* __restrict__ x_scale, int M, int K, const uint8_t* __restrict__ wq,
     const float* __restrict__ w_scale, int N, const float* __restrict__ bias, void* __restrict__ y) {
   using TL = Tile<BM, BN, WM, WN, NST>;
-  constexpr int FM = TL::FM, FN = TL::FN;
+  constexpr int AF = TL::AF, BF = TL::BF, H = TL::H;
+  static_assert(AF % 2 == 0 && TL::TN <= kScaleBlock, "wave tile");
   __shared__ __attribute__((aligned(16))) uint8_t smem[TL::kLds];
   float* const ssc = (float*)(smem + NST * TL::kStage);
   const int tid = threadIdx.x, lane = tid & 63;
@@ -207,73 +211,101 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     if (tid < BM) ssc[(j % NST) * BM + tid] = x_scale[(int64_t)j * M + (m0 + tid < M ? m0 + tid : M - 1)];
   };
 
-  v16f acc[FM][FN];
+  v4f acc[AF][BF];
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+  for (int i = 0; i < AF; ++i)
 #pragma unroll
-    for (int f = 0; f < FN; ++f) acc[i][f] = v16f{};
+    for (int f = 0; f < BF; ++f) acc[i][f] = v4f{0, 0, 0, 0};
 
-  const int lm = lane & 31, lh = lane >> 5;
-  // operand of row base + lane % 32, k-step ks: logical chunks 4 ks + 2 (lane / 32) + {0, 1}
-  const int lo = ((2 * lh) ^ swz_key(lm)) << 4;
-  auto frag = [&](const uint8_t* row, int ks) {
-    const v4i a = *(const v4i*)(row + (lo ^ (ks << 6))), b = *(const v4i*)(row + ((lo ^ 16) ^ (ks << 6)));
+  // operand of row base + lane % 16: logical chunks lane / 16 and lane / 16 + 4 (any split of the block
+  // does that both operands share).  A ds_read_b128 serves lanes 0-3, 12-15, 20-23 and 24-27 in one
+  // cycle: rows 0-3 and 12-15 of one chunk with rows 4-11 of the next are all 64 banks once; with
+  // chunks 2 (lane / 16) and 2 (lane / 16) + 1 every read took two turns.
+  const int lr = lane & 15, lg = lane >> 4;
+  const int lo = lr * kBK + ((lg ^ swz_key(lr)) << 4), lo2 = lo ^ 64;
+  const uint8_t* const sx_rows = smem + wm * TL::TM * kBK;
+  const uint8_t* const sw_rows = smem + (BM + wn * TL::TN) * kBK;
+  auto frag = [&](const uint8_t* rows) {
+    const v4i a = *(const v4i*)(rows + lo), b = *(const v4i*)(rows + lo2);
     return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   };
-  const float* wsc[FN];
-#pragma unroll
-  for (int f = 0; f < FN; ++f) {
-    const int n = n0 + wn * TL::TN + 32 * f;
-    wsc[f] = w_scale + (int64_t)((n < N ? n : N - 1) / kScaleBlock) * groups;
-  }
+  // the wave's columns lie in one block of 128 weight rows
+  const int nw = n0 + wn * TL::TN < N ? n0 + wn * TL::TN : N - 1;
+  const float* const wsc = w_scale + (int64_t)(nw / kScaleBlock) * groups;
 
-  // The fragments of a block: the weights' (kept over the block) and one row fragment's at a time,
-  // whose LDS reads run behind the FMAs of the fragment before.
-  float sw[FN], swn[FN], sx;
-  v8i fb[FN][2], fa[2];
-  auto load_b = [&](int j) {
-    const uint8_t* const wb = smem + (j % NST) * TL::kStage + (BM + wn * TL::TN + lm) * kBK;
+  // The block's weight fragments and half of its activation fragments are in registers; a fragment's
+  // registers are loaded again as soon as its last MFMA is issued, so LDS reads run all the time and a
+  // wave leaves the barrier with the second half of a block still to multiply.
+  float sw, swn, sx[H];
+  v8i fb[BF], fa[H];
+  auto load_b = [&](int slot, int f) { fb[f] = frag(sw_rows + slot * TL::kStage + f * 16 * kBK); };
+  auto load_a = [&](int slot, int h, int i) {
+    fa[h] = frag(sx_rows + slot * TL::kStage + i * 16 * kBK);
+    sx[h] = ssc[slot * BM + wm * TL::TM + 16 * i + lr];
+  };
+  auto mma = [&](int f, int h) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[f], fa[h], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+  };
+  auto add = [&](int i, int f, float s, const v4f p) {
 #pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      fb[f][0] = frag(wb + f * 32 * kBK, 0);
-      fb[f][1] = frag(wb + f * 32 * kBK, 1);
+    for (int r = 0; r < 4; ++r) acc[i][f][r] = __builtin_fmaf(s, p[r], acc[i][f][r]);
+  };
+  // Block j; `next` (uniform) runs once this wave has read all of it, and returns whether the
+  // registers are to be filled from the next slot.
+  auto block = [&](int slot, auto NEXT, auto&& next) {
+    constexpr bool more = decltype(NEXT)::value;
+    sw = swn;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      v4f p[BF];
+#pragma unroll
+      for (int f = 0; f < BF; ++f) p[f] = mma(f, h);
+      const float s = sx[h] * sw;
+      __builtin_amdgcn_sched_barrier(0);
+      load_a(slot, h, H + h);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = 0; f < BF; ++f) add(h, f, s, p[f]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  auto load_a = [&](int j, int i) {
-    const uint8_t* const xa = smem + (j % NST) * TL::kStage + (wm * TL::TM + lm + 32 * i) * kBK;
-    fa[0] = frag(xa, 0);
-    fa[1] = frag(xa, 1);
-  };
-  auto load_s = [&](int j) {
+    const int to = next();
+    float s[H];
 #pragma unroll
-    for (int f = 0; f < FN; ++f) swn[f] = wsc[f][j];
-  };
-  // Block j; `next` (uniform) runs once this wave has read all of it, between the last MFMAs and their FMAs.
-  auto block = [&](int j, auto&& next) {
+    for (int h = 0; h < H; ++h) s[h] = sx[h] * sw;
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sw[f] = swn[f];
+    for (int d = 0; d < (H > BF ? H : BF); ++d) {
+      v4f p[H], q[BF];
+      if (d < BF) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      sx = ssc[(j % NST) * BM + wm * TL::TM + 32 * i + lm];
-      v16f part[FN];
-#pragma unroll
-      for (int f = 0; f < FN; ++f)
-        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][0], fa[0], v16f{}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-      for (int f = 0; f < FN; ++f)
-        part[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f][1], fa[1], part[f], 0, 0, 0, 0, 0, 0);
+        for (int h = d; h < H; ++h) p[h] = mma(d, h);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) load_b(to, d);
+      }
       __builtin_amdgcn_sched_barrier(0);
-      if (i + 1 < FM) load_a(j, i + 1);
-      else next();
+      if (d < H) {
+#pragma unroll
+        for (int f = d + 1; f < BF; ++f) q[f] = mma(f, d);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) load_a(to, d, d);
+      }
       __builtin_amdgcn_sched_barrier(0);
+      if (d < BF) {
 #pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const float s = sx * sw[f];
+        for (int h = d; h < H; ++h) add(H + h, d, s[h], p[h]);
+      }
+      if (d < H) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][f][r] = __builtin_fmaf(s, part[f][r], acc[i][f][r]);
+        for (int f = d + 1; f < BF; ++f) add(H + d, f, s[d], q[f]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  auto load_all = [&](int slot, int j) {
+#pragma unroll
+    for (int f = 0; f < BF; ++f) load_b(slot, f);
+#pragma unroll
+    for (int h = 0; h < H; ++h) load_a(slot, h, h);
+    swn = wsc[j];
   };
 
   // All NST buffers are filled ahead, a buffer again as soon as every wave has read its block.  Past
@@ -291,17 +323,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     for (int b = 0; b < NST - 1; ++b) dma(clamped(b), b);
     arrived();
     dma(clamped(NST - 1), NST - 1);
-    load_b(0);
-    load_a(0, 0);
-    load_s(0);
+    load_all(0, 0);
     for (; j + 1 < full; ++j)
-      block(j, [&] {
+      block(j % NST, std::true_type{}, [&] {
         __builtin_amdgcn_s_waitcnt(kLgkmcnt0);          // this wave's reads of block j are done
         arrived();
         dma(clamped(j + NST), j % NST);
-        load_b(j + 1);
-        load_a(j + 1, 0);
-        load_s(j + 1);
+        swn = wsc[j + 1];
+        return (j + 1) % NST;
       });
   }
   for (; j < groups; ++j) {
@@ -310,18 +339,16 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
       __syncthreads();
       tail(j);
       __syncthreads();
-      load_b(j);
-      load_a(j, 0);
-      load_s(j);
+      load_all(j % NST, j);
     }
-    block(j, [] {});
+    block(j % NST, std::false_type{}, [] { return 0; });
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // repeated blocks still on their way
 
-  // epilogue: one 32-row slab of a wave at a time through padded LDS, back row-contiguous, 8 columns a lane
+  // epilogue: one 16-row slab of a wave at a time through padded LDS, back row-contiguous, 8 columns a lane
   __syncthreads();
   constexpr int kPitch = TL::kPitch, LPR = TL::TN / 8, RPI = 64 / LPR;
-  uint8_t* const stg = smem + wave * 32 * kPitch;
+  uint8_t* const stg = smem + wave * 16 * kPitch;
   const int rc = lane % LPR, rr = lane / LPR;
   const int n = n0 + wn * TL::TN + 8 * rc;
   float b8[8];
@@ -329,18 +356,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
   for (int e = 0; e < 8; ++e) b8[e] = bias && n + e < N ? bias[n + e] : 0.0f;
   const bool vec = (N & 7) == 0;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  for (int i = 0; i < AF; ++i) {
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+    for (int f = 0; f < BF; ++f) *(v4f*)(stg + lr * kPitch + (16 * f + 4 * lg) * 4) = acc[i][f];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(v4f*)(stg + lm * kPitch + (32 * f + 8 * q + 4 * lh) * 4) =
-            v4f{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
-#pragma unroll
-    for (int t = 0; t < 32 / RPI; ++t) {
-      const int row = t * RPI + rr, m = m0 + wm * TL::TM + 32 * i + row;
+    for (int t = 0; t < (16 + RPI - 1) / RPI; ++t) {
+      const int row = t * RPI + rr, m = m0 + wm * TL::TM + 16 * i + row;
+      if (row >= 16 || m >= M || n >= N) continue;
       const v4f a = *(const v4f*)(stg + row * kPitch + rc * 32), b = *(const v4f*)(stg + row * kPitch + rc * 32 + 16);
-      if (m >= M || n >= N) continue;
       const float v[8] = {a[0] + b8[0], a[1] + b8[1], a[2] + b8[2], a[3] + b8[3],
                           b[0] + b8[4], b[1] + b8[5], b[2] + b8[6], b[3] + b8[7]};
       uint16_t* const o = (uint16_t*)y + (int64_t)m * N + n;
