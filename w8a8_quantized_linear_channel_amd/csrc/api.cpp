@@ -166,7 +166,7 @@ q8_status check_kv(int64_t T, int64_t Hkv, int64_t D, int64_t S, int64_t max_pag
     return Q8_ERR_BAD_SHAPE;
   if (D != 64 && D != 128 && D != 256) return Q8_ERR_BAD_SHAPE;
   if (page != 32 && page != 64 && page != 128) return Q8_ERR_BAD_SHAPE;
-  if (num_pages < 1 || num_pages > kMaxRows || max_pages < 1 || max_pages > kMaxRows / page - 256)
+  if (num_pages < 1 || num_pages * Hkv > kMaxRows || num_pages > kMaxRows || max_pages < 1 || max_pages > kMaxRows / page - 256)
     return Q8_ERR_BAD_SHAPE;
   return Q8_OK;
 }

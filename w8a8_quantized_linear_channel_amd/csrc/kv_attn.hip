@@ -305,6 +305,310 @@ __global__ __launch_bounds__(kThreads) void k_attn_rows(const AttnArgs a, int ro
   }
 }
 
+// ---------------------------------------------------------------- many rows
+// A workgroup takes 128 rows of one sequence and kv head, 32 a wave, and goes
+// through the keys in steps of 64 that it brings into LDS as codes (DMA, three
+// steps ahead).  v_mfma_f32_32x32x16: S^T = K Q^T in two 32-key tiles, lane
+// (q, h) (q = lane % 32, h = lane / 32) holding row q; tile T's row 8 a + 4 h + b
+// is key 32 h + 16 T + 4 a + b, so that register i of tile T is key 32 h + 16 T
+// + i and the weights are the B operand of O^T = V^T P^T as they stand.  Each
+// wave widens the codes it reads; two workgroups share a CU, so one wave's
+// softmax runs beside another's MFMAs.
+//
+// The running maximum is a reference that is only moved when a score passes it
+// by 2^8 (weights up to 256 fit f16 and cost no precision): most steps neither
+// rescale nor exchange anything between lanes.
+typedef float v16 __attribute__((ext_vector_type(16)));
+constexpr int kStep = 64;        // keys of one step
+constexpr int kStages = 4;       // steps in LDS
+constexpr int kBlockRows = 128;
+constexpr int kMeta = kThreads;  // 32-key halves whose page and exponents are held at a time
+
+template <int DT>
+__device__ __forceinline__ v16 mma32(const v4i a, const v4i b, const v16 c) {
+  if constexpr (DT == DT_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// 16-byte chunk c of a key's D bytes sits at chunk c ^ key_swz: the 16 lanes that a ds_read_b128
+// serves in one cycle (0-3, 12-15, 20-23, 24-27 and their complements) read 16 keys of one chunk.
+template <int D>
+__device__ __forceinline__ int key_swz(int key) { return D == 64 ? (key >> 2) & 3 : D == 128 ? (key >> 1) & 7 : key & 15; }
+// the same of a feature's 64 value bytes
+__device__ __forceinline__ int val_swz(int d) { return (d >> 2) & 3; }
+
+template <int D, int DT>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attn_tiles(const AttnArgs a, int row_tiles, int splits,
+                                                                          int chunk) {
+  constexpr int KS = D / 16;                     // MFMA steps over the features
+  constexpr int NT = D / 32;                     // 32-feature tiles of the output
+  constexpr int kTileBytes = kStep * D;          // of keys, and of values
+  constexpr int kLoads = kTileBytes / 1024 / kWaves;   // DMAs of a wave for each
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kStages * 2 * kTileBytes];
+  // page times heads plus head, and the exponent bytes (keys | values << 8), of each 32-key half of
+  // up to kMeta / 2 steps: read once, so that the loop's only global loads are its DMAs
+  __shared__ int s_page[kMeta], s_exp[kMeta];
+  const KvView& kv = a.kv;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 31, lh = lane >> 5;
+  // one kv head's workgroups on one XCD where the heads allow it (the dispatcher deals workgroups
+  // round-robin over the XCDs), the longest rows first
+  int b = blockIdx.x;
+  const int head = b % kv.kv_heads;
+  b /= kv.kv_heads;
+  const int split = b % splits;
+  b /= splits;
+  const int s = b % kv.seqs, tile0 = b / kv.seqs;
+  const int group = a.heads / kv.kv_heads;
+  const Span sp = span_of(a, s);
+  const int rows = sp.n * group;
+  const int tiles = (rows + kBlockRows - 1) / kBlockRows;
+
+  for (int tile = tiles - 1 - tile0; tile >= 0; tile -= row_tiles) {
+    const int r0 = tile * kBlockRows;
+    // this lane's row (rows past the end repeat the last one and are not stored)
+    const int row = r0 + 32 * wave + lr, rc = row < rows ? row : rows - 1;
+    const int tok = rc / group, hq = rc - tok * group;
+    const int pos = sp.past + tok;
+    const int high = a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total;
+    const int low = a.window > 0 ? pos - a.window + 1 : 0;
+    v4i qf[KS];
+    {
+      const uint16_t* q = (const uint16_t*)a.q + (int64_t)(sp.first + tok) * a.q_stride +
+                          (int64_t)(head * group + hq) * D + lh * (D / 2);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[ks] = *(const v4i*)(q + 8 * ks);
+        if (a.scale_log2 < 0.0f) qf[ks] ^= (int)0x80008000u;      // the sign of the scale goes into q
+      }
+    }
+    const float scale = fabsf(a.scale_log2);
+    // keys that any row of the block sees, and the range in which every row of the wave sees every key
+    const int last = (r0 + kBlockRows < rows ? r0 + kBlockRows : rows) - 1;
+    const int p0 = sp.past + r0 / group, p1 = sp.past + last / group;
+    const int klo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+    const int khi = a.causal ? (p1 + 1 < sp.total ? p1 + 1 : sp.total) : sp.total;
+    const int w0 = r0 + 32 * wave < rows ? r0 + 32 * wave : rows - 1;
+    const int w1 = w0 + 31 < rows ? w0 + 31 : rows - 1;
+    const int pw0 = sp.past + w0 / group, pw1 = sp.past + w1 / group;
+    const int all_hi = __builtin_amdgcn_readfirstlane(a.causal ? (pw0 + 1 < sp.total ? pw0 + 1 : sp.total) : sp.total);
+    const int all_lo = __builtin_amdgcn_readfirstlane(a.window > 0 ? pw1 - a.window + 1 : 0);
+    const int base = klo & ~(kStep - 1);
+    const int64_t from = (int64_t)split * chunk;
+    const int kb0 = base + from < khi ? base + (int)from : khi;
+    const int kb1 = split + 1 < splits && kb0 + (int64_t)chunk < khi ? kb0 + chunk : khi;
+    const int steps = (kb1 - kb0 + kStep - 1) / kStep;
+
+    // the lane's place in the DMAs: instruction j (0 .. 4 kLoads - 1) of a tile fills 1 KB
+    uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+    for (int d = 0; d < kLoads; ++d) {
+      const int slot = (d * kWaves + wave) * 64 + lane;
+      const int key = slot / (D / 16), f = slot / 4;
+      koff[d] = (uint32_t)((key & 31) * D + (((slot % (D / 16)) ^ key_swz<D>(key)) << 4));
+      voff[d] = (uint32_t)(f * kv.page) + ((uint32_t)(slot & 1) << 4 ^ (uint32_t)(val_swz(f) & 1) << 4);
+    }
+    // which 32-key half of the step the lane's value chunk belongs to (the same for every d)
+    const bool vhalf = (((lane & 3) ^ val_swz(lane >> 2)) >> 1) != 0;
+    // step i of the run of `n` that s_page describes; past its end the last one again
+    auto dma = [&](int i, int n, int kb_run) {
+      uint8_t* const st = smem + (i % kStages) * 2 * kTileBytes;
+      i = i < n ? i : n - 1;
+      const int kb = kb_run + i * kStep;
+      const int ph0 = __builtin_amdgcn_readfirstlane(s_page[2 * i]), ph1 = __builtin_amdgcn_readfirstlane(s_page[2 * i + 1]);
+      const int64_t o0 = kb & (kv.page - 1), o1 = (kb + 32) & (kv.page - 1);
+#pragma unroll
+      for (int d = 0; d < kLoads; ++d) {
+        const bool second = (d * kWaves + wave) * (1024 / D) >= 32;
+        const uint8_t* p = kv.k + ((int64_t)(second ? ph1 : ph0) * kv.page + (second ? o1 : o0)) * D;
+        dma16(p, koff[d], st + (d * kWaves + wave) * 1024);
+      }
+      const uint8_t* const b0 = kv.v + (int64_t)ph0 * D * kv.page + o0;
+      const uint8_t* const b1 = kv.v + (int64_t)ph1 * D * kv.page + o1;
+      const uint8_t* const bv = vhalf ? b1 : b0;
+#pragma unroll
+      for (int d = 0; d < kLoads; ++d) dma16_ptr(bv + voff[d], st + kTileBytes + (d * kWaves + wave) * 1024);
+    };
+
+    v16 acc[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n] = v16{};
+    float m = -INFINITY, l = 0.0f;
+    int bmax = 0;
+
+    // operand row of key tile T: LDS key 32 h' + 16 T + 4 a + b of row 8 a + 4 h' + b
+    const int key0 = 32 * ((lr >> 2) & 1) + 4 * (lr >> 3) + (lr & 3);
+    const int kswz = key_swz<D>(key0);             // the same for both tiles
+    auto step = [&](int i, int kb) {
+      const uint8_t* const st = smem + (i % kStages) * 2 * kTileBytes;
+      const int ex0 = __builtin_amdgcn_readfirstlane(s_exp[2 * i]), ex1 = __builtin_amdgcn_readfirstlane(s_exp[2 * i + 1]);
+      const int v0 = ex0 >> 8, v1 = ex1 >> 8;
+      // not 0: a masked score of -inf stays one
+      const float kscale = fmaxf(exp_byte((lh ? ex1 : ex0) & 255) * scale, 1.17549435e-38f);
+      v16 sc[2];
+      v4i kx[2][D / 32];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          kx[t][c] = *(const v4i*)(st + (key0 + 16 * t) * D + (((lh * (D / 32) + c) ^ kswz) << 4));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        sc[t] = v16{};
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          sc[t] = mma32<DT>(widen8<DT>(kx[t][c][0], kx[t][c][1], 1.0f), qf[2 * c], sc[t]);
+          sc[t] = mma32<DT>(widen8<DT>(kx[t][c][2], kx[t][c][3], 1.0f), qf[2 * c + 1], sc[t]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const int keyv = kb + 32 * lh;
+      if (!(kb >= all_lo && kb + kStep <= all_hi)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int key = keyv + 16 * t + r;
+            sc[t][r] = key >= low && key < high ? sc[t][r] : -INFINITY;
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[t][r]);
+      mx *= kscale;
+      const int bt = v0 > v1 ? v0 : v1;
+      if (__any(mx > m + 8.0f) || bt > bmax) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float mn = fmaxf(m, mx);
+        const int bn = bt > bmax ? bt : bmax;
+        int down = bmax - bn;
+        down = down < -126 ? -126 : down;
+        const float alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        m = mn;
+        bmax = bn;
+        l *= alpha;
+        const float fix = alpha * __builtin_ldexpf(1.0f, down);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] *= fix;
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      v4i pf[4];
+      float sum = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          sc[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], kscale, -ref));
+          sum += sc[t][r];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          pf[2 * t + j] = v4i{(int)pack2_out<DT_F16>(sc[t][8 * j], sc[t][8 * j + 1]),
+                              (int)pack2_out<DT_F16>(sc[t][8 * j + 2], sc[t][8 * j + 3]),
+                              (int)pack2_out<DT_F16>(sc[t][8 * j + 4], sc[t][8 * j + 5]),
+                              (int)pack2_out<DT_F16>(sc[t][8 * j + 6], sc[t][8 * j + 7])};
+      }
+      l += sum;
+      int down = (lh ? v1 : v0) - bmax;
+      down = down < -126 ? -126 : down;
+      const float vscale = __builtin_ldexpf(1.0f, down);
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t* const vr = st + kTileBytes + lr * 64;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        v4i x[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) x[t] = *(const v4i*)(vr + n * 2048 + (((2 * lh + t) ^ val_swz(lr)) << 4));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          acc[n] = mma32<DT_F16>(widen8<DT_F16>(x[t][0], x[t][1], vscale), pf[2 * t], acc[n]);
+          acc[n] = mma32<DT_F16>(widen8<DT_F16>(x[t][2], x[t][3], vscale), pf[2 * t + 1], acc[n]);
+        }
+      }
+    };
+    // Value codes of keys that no row sees are cleared in LDS (they may be anything, NaN codes
+    // included; their scores are masked).  Uniform over the workgroup.
+    auto clear = [&](int i, int kb) {
+      uint8_t* const st = smem + (i % kStages) * 2 * kTileBytes + kTileBytes;
+      for (int slot = tid; slot < D * 4; slot += kThreads) {
+        const int f = slot >> 2, key = kb + 16 * ((slot & 3) ^ val_swz(f));
+        v4i x = *(const v4i*)(st + slot * 16);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) keep |= key + 4 * w + e >= klo && key + 4 * w + e < khi ? 0xffu << (8 * e) : 0u;
+          x[w] &= (int)keep;
+        }
+        *(v4i*)(st + slot * 16) = x;
+      }
+      __syncthreads();
+    };
+
+    for (int run = 0; run < steps; run += kMeta / 2) {
+      const int n = steps - run < kMeta / 2 ? steps - run : kMeta / 2;
+      const int kb_run = kb0 + run * kStep;
+      {
+        // a half that no row sees reads page 0 and counts as values of exponent 0
+        const int key = kb_run + 32 * tid;
+        const bool seen = key < khi && key + 32 > klo;
+        int p = seen ? kv.table[(int64_t)s * kv.max_pages + key / kv.page] : 0;
+        p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
+        p = p * kv.kv_heads + head;
+        s_page[tid] = p;
+        s_exp[tid] = kv.ke[p] | (seen ? kv.ve[p] << 8 : 0);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) dma(i, n, kb_run);
+      for (int i = 0; i < n; ++i) {
+        // step i is this wave's oldest stage in LDS; two later ones may be on their way (past the last
+        // step the DMA repeats it, so that the count is always the same)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 2) * 2 * kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();              // and every wave is past step i - 1
+        asm volatile("" ::: "memory");
+        dma(i + kStages - 1, n, kb_run);
+        const int kb = kb_run + i * kStep;
+        if (kb < klo || kb + kStep > khi) clear(i, kb);
+        step(i, kb);
+        __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32);
+    if (row < rows) {
+      const float vtrue = exp_byte(bmax);
+      const int64_t orow = (int64_t)(sp.first + tok) * a.heads + head * group + hq;
+      const float inv = (splits > 1 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f)) * vtrue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const int d = 32 * n + 2 * r + 4 * lh;
+          const v4f o = {acc[n][r] * inv, acc[n][r + 1] * inv, acc[n][r + 2] * inv, acc[n][r + 3] * inv};
+          if (splits > 1) *(v4f*)(a.part + ((int64_t)split * kv.tokens * a.heads + orow) * D + d) = o;
+          else *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
+        }
+      if (lh == 0) {
+        if (splits > 1) {
+          float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
+          ml[0] = m;
+          ml[1] = l;
+        } else if (a.lse) {
+          a.lse[orow] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+    }
+  }
+}
+
 // Joins the splits of a row, in their order: one wave per row of a sequence.
 template <int D, int DT>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks, int splits) {
@@ -336,15 +640,21 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks,
   }
 }
 
-constexpr int kSmallRows = 16;      // rows of one workgroup: one row tile
-constexpr int kManyRows = 64;       // four row tiles
+constexpr int kSmallRows = 16;      // up to here one 16-row tile, above 128-row blocks
 
-// Keys of one split and the number of splits.
-void split_plan(int64_t rows, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window, int* splits, int* chunk) {
+// How a call is cut: rows of one workgroup, row blocks of a sequence, splits of the keys and keys of
+// one split.
+struct Plan {
+  int64_t per, blocks;
+  int splits, chunk;
+};
+Plan plan_of(int64_t rows, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
+  Plan p;
+  p.per = rows > kSmallRows ? kBlockRows : kSmallRows;
+  p.blocks = (rows + p.per - 1) / p.per;
   int64_t keys = max_kv;
   if (window > 0 && window + max_q + kTile < keys) keys = window + max_q + kTile;
-  const int64_t per = rows > kSmallRows ? kManyRows : kSmallRows;
-  const int64_t groups = (int64_t)seqs * kv_heads * ((rows + per - 1) / per);
+  const int64_t groups = (int64_t)seqs * kv_heads * p.blocks;
   const int64_t step = kWaves * kTile;
   int64_t want = (1024 + groups - 1) / groups;
   const int64_t most = (keys + step - 1) / step;
@@ -352,29 +662,33 @@ void split_plan(int64_t rows, int kv_heads, int seqs, int64_t max_q, int64_t max
   want = want < 1 ? 1 : want;
   int64_t c = ((keys + want - 1) / want + step - 1) / step * step;
   c = c < step ? step : c;
-  *splits = (int)((keys + c - 1) / c);
-  if (*splits < 1) *splits = 1;
-  *chunk = (int)c;
+  p.splits = (int)((keys + c - 1) / c);
+  if (p.splits < 1) p.splits = 1;
+  p.chunk = (int)c;
+  const int64_t most_blocks = ((int64_t)1 << 30) / ((int64_t)seqs * kv_heads * p.splits);
+  if (p.per == kSmallRows && p.blocks > 65535 / seqs) p.blocks = 65535 / seqs;
+  if (p.blocks > most_blocks) p.blocks = most_blocks;
+  if (p.blocks < 1) p.blocks = 1;
+  return p;
 }
 
 template <int D, int DT>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.heads / a.kv.kv_heads);
-  int splits = 1, chunk = kTile;
-  split_plan(rows, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window, &splits, &chunk);
-  const int64_t per = rows > kSmallRows ? kManyRows : kSmallRows;
-  int64_t tiles = (rows + per - 1) / per;
-  const int64_t most = 65535 / a.kv.seqs;
-  tiles = tiles > most ? (most < 1 ? 1 : most) : tiles;
-  const dim3 grid((unsigned)splits, (unsigned)a.kv.kv_heads, (unsigned)(tiles * a.kv.seqs));
-  if (per == kSmallRows) k_attn_rows<D, 1, DT><<<grid, kThreads, 0, st>>>(a, (int)tiles, chunk);
-  else k_attn_rows<D, 4, DT><<<grid, kThreads, 0, st>>>(a, (int)tiles, chunk);
+  const Plan p = plan_of(rows, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
+  if (p.per == kSmallRows) {
+    const dim3 grid((unsigned)p.splits, (unsigned)a.kv.kv_heads, (unsigned)(p.blocks * a.kv.seqs));
+    k_attn_rows<D, 1, DT><<<grid, kThreads, 0, st>>>(a, (int)p.blocks, p.chunk);
+  } else {
+    const unsigned grid = (unsigned)(p.blocks * a.kv.seqs * a.kv.kv_heads * p.splits);
+    k_attn_tiles<D, DT><<<grid, kThreads, 0, st>>>(a, (int)p.blocks, p.splits, p.chunk);
+  }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
+  if (e != hipSuccess || p.splits == 1) return e;
   int64_t blocks = ((int64_t)a.max_q * a.heads + 3) / 4;
   const int64_t limit = ((int64_t)1 << 30) / a.kv.seqs;
   blocks = blocks > limit ? limit : blocks;
-  k_attn_join<D, DT><<<(unsigned)(blocks * a.kv.seqs), 256, 0, st>>>(a, (int)blocks, splits);
+  k_attn_join<D, DT><<<(unsigned)(blocks * a.kv.seqs), 256, 0, st>>>(a, (int)blocks, p.splits);
   return hipGetLastError();
 }
 template <int DT>
@@ -390,9 +704,7 @@ hipError_t launch_dt(const AttnArgs& a, int dim, hipStream_t st) {
 
 int attn_splits(int64_t tokens, int heads, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
   (void)tokens;
-  int splits = 1, chunk = 0;
-  split_plan(max_q * (heads / kv_heads), kv_heads, seqs, max_q, max_kv, window, &splits, &chunk);
-  return splits;
+  return plan_of(max_q * (heads / kv_heads), kv_heads, seqs, max_q, max_kv, window).splits;
 }
 
 hipError_t launch_attention(const AttnArgs& a, int dt, int dim, hipStream_t st) {
