@@ -197,7 +197,7 @@ struct AttnWs { size_t part, ml, total; };
 AttnWs attn_ws(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q, int64_t max_kv, int64_t window) {
   AttnWs w{0, 0, 0};
   if (T == 0) return w;
-  const int64_t splits = q8::attn_splits(T, (int)Hq, (int)Hkv, (int)S, max_q, max_kv, (int)window);
+  const int64_t splits = q8::attn_splits((int)Hq, (int)Hkv, (int)D, (int)S, max_q, max_kv, (int)window);
   if (splits <= 1) return w;
   Carve c;
   w.part = c.take((size_t)splits * T * Hq * D * 4);

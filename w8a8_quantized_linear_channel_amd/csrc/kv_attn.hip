@@ -18,6 +18,9 @@
 // exponent byte seen so far (f16 holds 2^-24 .. 65504), which the accumulator
 // is rescaled to; the softmax weights are rounded to f16 (2^-12 of a weight),
 // and maximum, sum and accumulator are held in 32 bits.
+#include <type_traits>
+#include <utility>
+
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
 
@@ -306,23 +309,24 @@ __global__ __launch_bounds__(kThreads) void k_attn_rows(const AttnArgs a, int ro
 }
 
 // ---------------------------------------------------------------- many rows
-// A workgroup takes 128 rows of one sequence and kv head, 32 a wave, and goes
-// through the keys in steps of 64 that it brings into LDS as codes (DMA, three
-// steps ahead).  v_mfma_f32_32x32x16: S^T = K Q^T in two 32-key tiles, lane
-// (q, h) (q = lane % 32, h = lane / 32) holding row q; tile T's row 8 a + 4 h + b
-// is key 32 h + 16 T + 4 a + b, so that register i of tile T is key 32 h + 16 T
-// + i and the weights are the B operand of O^T = V^T P^T as they stand.  Each
-// wave widens the codes it reads; two workgroups share a CU, so one wave's
-// softmax runs beside another's MFMAs.
+// A workgroup of NW waves takes 32 NW rows of one sequence and kv head, 32 a
+// wave, and goes through the keys in steps of 64.  The codes of a step are read
+// once, two steps ahead, widened by the thread that read them and put into
+// LDS (two buffers), from where every wave reads MFMA operands; widened by each
+// wave for itself the conversions are a third of all vector instructions
+// (675 against 4xx us for a prompt of 8192 tokens, 32 heads over 8).
+//
+// v_mfma_f32_32x32x16: S^T = K Q^T in two 32-key tiles, lane (q, h) (q = lane %
+// 32, h = lane / 32) holding row q; tile T's row 8 a + 4 h + b is key 32 h +
+// 16 T + 4 a + b, so that register i of tile T is key 32 h + 16 T + i and the
+// weights are the B operand of O^T = V^T P^T as they stand.
 //
 // The running maximum is a reference that is only moved when a score passes it
 // by 2^8 (weights up to 256 fit f16 and cost no precision): most steps neither
 // rescale nor exchange anything between lanes.
 typedef float v16 __attribute__((ext_vector_type(16)));
 constexpr int kStep = 64;        // keys of one step
-constexpr int kStages = 4;       // steps in LDS
-constexpr int kBlockRows = 128;
-constexpr int kMeta = kThreads;  // 32-key halves whose page and exponents are held at a time
+constexpr int kMeta = 256;       // 32-key halves whose page and exponents are held at a time
 
 template <int DT>
 __device__ __forceinline__ v16 mma32(const v4i a, const v4i b, const v16 c) {
@@ -332,24 +336,39 @@ __device__ __forceinline__ v16 mma32(const v4i a, const v4i b, const v16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// 16-byte chunk c of a key's D bytes sits at chunk c ^ key_swz: the 16 lanes that a ds_read_b128
-// serves in one cycle (0-3, 12-15, 20-23, 24-27 and their complements) read 16 keys of one chunk.
-template <int D>
-__device__ __forceinline__ int key_swz(int key) { return D == 64 ? (key >> 2) & 3 : D == 128 ? (key >> 1) & 7 : key & 15; }
-// the same of a feature's 64 value bytes
-__device__ __forceinline__ int val_swz(int d) { return (d >> 2) & 3; }
+// f(0) .. f(N - 1) with the number as a type: what it indexes stays in registers
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) { each_of(f, std::make_integer_sequence<int, N>{}); }
 
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attn_tiles(const AttnArgs a, int row_tiles, int splits,
-                                                                          int chunk) {
+// b where `mask` is all ones, a where it is 0 (a select the compiler cannot turn into an indexed read)
+__device__ __forceinline__ int pick(int mask, int a, int b) { return (a & ~mask) | (b & mask); }
+
+// LDS places of the widened operands: 16-byte chunk c of a key's 2 D bytes (of a feature's 128 bytes
+// of values) sits at chunk c ^ key_swz (val_swz), so that the 16 lanes that a ds_read_b128 serves in
+// one cycle (0-3, 12-15, 20-23, 24-27 and their complements) cover all 64 banks once.
+template <int D>
+__device__ __forceinline__ constexpr int key_swz(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
+__device__ __forceinline__ int val_swz(int d) { return (d >> 1) & 7; }
+
+template <int D, int DT, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const AttnArgs a, int row_tiles, int splits,
+                                                                         int chunk) {
+  constexpr int kThr = 64 * NW, kRows = 32 * NW;
   constexpr int KS = D / 16;                     // MFMA steps over the features
   constexpr int NT = D / 32;                     // 32-feature tiles of the output
-  constexpr int kTileBytes = kStep * D;          // of keys, and of values
-  constexpr int kLoads = kTileBytes / 1024 / kWaves;   // DMAs of a wave for each
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kStages * 2 * kTileBytes];
-  // page times heads plus head, and the exponent bytes (keys | values << 8), of each 32-key half of
-  // up to kMeta / 2 steps: read once, so that the loop's only global loads are its DMAs
-  __shared__ int s_page[kMeta], s_exp[kMeta];
+  constexpr int kTileBytes = kStep * D * 2;      // of widened keys, and of values
+  constexpr int kChunks = kStep * D / 16;        // 16-byte chunks of codes of a step's keys, and of its values
+  constexpr int kPer = 2 * kChunks / kThr;       // of a thread
+  static_assert(kPer >= 1 && 2 * kChunks % kThr == 0 && kChunks % 64 == 0, "load split");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * 2 * kTileBytes];
+  // byte offset of the page's head, and the exponent bytes (keys | values << 8), of each 32-key half
+  // of up to kMeta / 2 steps
+  __shared__ int64_t s_page[kMeta];
+  __shared__ int s_exp[kMeta], s_top[NW];
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -365,16 +384,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attn_tiles(const
   const int group = a.heads / kv.kv_heads;
   const Span sp = span_of(a, s);
   const int rows = sp.n * group;
-  const int tiles = (rows + kBlockRows - 1) / kBlockRows;
+  const int tiles = (rows + kRows - 1) / kRows;
 
   for (int tile = tiles - 1 - tile0; tile >= 0; tile -= row_tiles) {
-    const int r0 = tile * kBlockRows;
+    const int r0 = tile * kRows;
     // this lane's row (rows past the end repeat the last one and are not stored)
     const int row = r0 + 32 * wave + lr, rc = row < rows ? row : rows - 1;
     const int tok = rc / group, hq = rc - tok * group;
     const int pos = sp.past + tok;
-    const int high = a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total;
-    const int low = a.window > 0 ? pos - a.window + 1 : 0;
     v4i qf[KS];
     {
       const uint16_t* q = (const uint16_t*)a.q + (int64_t)(sp.first + tok) * a.q_stride +
@@ -386,206 +403,276 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attn_tiles(const
       }
     }
     const float scale = fabsf(a.scale_log2);
-    // keys that any row of the block sees, and the range in which every row of the wave sees every key
-    const int last = (r0 + kBlockRows < rows ? r0 + kBlockRows : rows) - 1;
+    // keys that any row of the block sees, and those that every row of the wave does
+    const int last = (r0 + kRows < rows ? r0 + kRows : rows) - 1;
     const int p0 = sp.past + r0 / group, p1 = sp.past + last / group;
     const int klo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
     const int khi = a.causal ? (p1 + 1 < sp.total ? p1 + 1 : sp.total) : sp.total;
     const int w0 = r0 + 32 * wave < rows ? r0 + 32 * wave : rows - 1;
     const int w1 = w0 + 31 < rows ? w0 + 31 : rows - 1;
     const int pw0 = sp.past + w0 / group, pw1 = sp.past + w1 / group;
-    const int all_hi = __builtin_amdgcn_readfirstlane(a.causal ? (pw0 + 1 < sp.total ? pw0 + 1 : sp.total) : sp.total);
-    const int all_lo = __builtin_amdgcn_readfirstlane(a.window > 0 ? pw1 - a.window + 1 : 0);
+    const int all_hi = a.causal ? (pw0 + 1 < sp.total ? pw0 + 1 : sp.total) : sp.total;
+    const int all_lo = a.window > 0 ? pw1 - a.window + 1 : 0;
     const int base = klo & ~(kStep - 1);
     const int64_t from = (int64_t)split * chunk;
     const int kb0 = base + from < khi ? base + (int)from : khi;
     const int kb1 = split + 1 < splits && kb0 + (int64_t)chunk < khi ? kb0 + chunk : khi;
     const int steps = (kb1 - kb0 + kStep - 1) / kStep;
 
-    // the lane's place in the DMAs: instruction j (0 .. 4 kLoads - 1) of a tile fills 1 KB
-    uint32_t koff[kLoads], voff[kLoads];
-#pragma unroll
-    for (int d = 0; d < kLoads; ++d) {
-      const int slot = (d * kWaves + wave) * 64 + lane;
-      const int key = slot / (D / 16), f = slot / 4;
-      koff[d] = (uint32_t)((key & 31) * D + (((slot % (D / 16)) ^ key_swz<D>(key)) << 4));
-      voff[d] = (uint32_t)(f * kv.page) + ((uint32_t)(slot & 1) << 4 ^ (uint32_t)(val_swz(f) & 1) << 4);
-    }
-    // which 32-key half of the step the lane's value chunk belongs to (the same for every d)
-    const bool vhalf = (((lane & 3) ^ val_swz(lane >> 2)) >> 1) != 0;
-    // step i of the run of `n` that s_page describes; past its end the last one again
-    auto dma = [&](int i, int n, int kb_run) {
-      uint8_t* const st = smem + (i % kStages) * 2 * kTileBytes;
-      i = i < n ? i : n - 1;
-      const int kb = kb_run + i * kStep;
-      const int ph0 = __builtin_amdgcn_readfirstlane(s_page[2 * i]), ph1 = __builtin_amdgcn_readfirstlane(s_page[2 * i + 1]);
-      const int64_t o0 = kb & (kv.page - 1), o1 = (kb + 32) & (kv.page - 1);
-#pragma unroll
-      for (int d = 0; d < kLoads; ++d) {
-        const bool second = (d * kWaves + wave) * (1024 / D) >= 32;
-        const uint8_t* p = kv.k + ((int64_t)(second ? ph1 : ph0) * kv.page + (second ? o1 : o0)) * D;
-        dma16(p, koff[d], st + (d * kWaves + wave) * 1024);
-      }
-      const uint8_t* const b0 = kv.v + (int64_t)ph0 * D * kv.page + o0;
-      const uint8_t* const b1 = kv.v + (int64_t)ph1 * D * kv.page + o1;
-      const uint8_t* const bv = vhalf ? b1 : b0;
-#pragma unroll
-      for (int d = 0; d < kLoads; ++d) dma16_ptr(bv + voff[d], st + kTileBytes + (d * kWaves + wave) * 1024);
-    };
-
     v16 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = v16{};
     float m = -INFINITY, l = 0.0f;
-    int bmax = 0;
+    int bmax = 0;                                // the values' reference exponent byte
 
-    // operand row of key tile T: LDS key 32 h' + 16 T + 4 a + b of row 8 a + 4 h' + b
-    const int key0 = 32 * ((lr >> 2) & 1) + 4 * (lr >> 3) + (lr & 3);
-    const int kswz = key_swz<D>(key0);             // the same for both tiles
-    auto step = [&](int i, int kb) {
-      const uint8_t* const st = smem + (i % kStages) * 2 * kTileBytes;
-      const int ex0 = __builtin_amdgcn_readfirstlane(s_exp[2 * i]), ex1 = __builtin_amdgcn_readfirstlane(s_exp[2 * i + 1]);
-      const int v0 = ex0 >> 8, v1 = ex1 >> 8;
-      // not 0: a masked score of -inf stays one
-      const float kscale = fmaxf(exp_byte((lh ? ex1 : ex0) & 255) * scale, 1.17549435e-38f);
-      v16 sc[2];
-      v4i kx[2][D / 32];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          kx[t][c] = *(const v4i*)(st + (key0 + 16 * t) * D + (((lh * (D / 32) + c) ^ kswz) << 4));
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        sc[t] = v16{};
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          sc[t] = mma32<DT>(widen8<DT>(kx[t][c][0], kx[t][c][1], 1.0f), qf[2 * c], sc[t]);
-          sc[t] = mma32<DT>(widen8<DT>(kx[t][c][2], kx[t][c][3], 1.0f), qf[2 * c + 1], sc[t]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      const int keyv = kb + 32 * lh;
-      if (!(kb >= all_lo && kb + kStep <= all_hi)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int key = keyv + 16 * t + r;
-            sc[t][r] = key >= low && key < high ? sc[t][r] : -INFINITY;
-          }
-      }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[t][r]);
-      mx *= kscale;
-      const int bt = v0 > v1 ? v0 : v1;
-      if (__any(mx > m + 8.0f) || bt > bmax) {
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m, mx);
-        const int bn = bt > bmax ? bt : bmax;
-        int down = bmax - bn;
-        down = down < -126 ? -126 : down;
-        const float alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
-        m = mn;
-        bmax = bn;
-        l *= alpha;
-        const float fix = alpha * __builtin_ldexpf(1.0f, down);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] *= fix;
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      v4i pf[4];
-      float sum = 0.0f;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          sc[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], kscale, -ref));
-          sum += sc[t][r];
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          pf[2 * t + j] = v4i{(int)pack2_out<DT_F16>(sc[t][8 * j], sc[t][8 * j + 1]),
-                              (int)pack2_out<DT_F16>(sc[t][8 * j + 2], sc[t][8 * j + 3]),
-                              (int)pack2_out<DT_F16>(sc[t][8 * j + 4], sc[t][8 * j + 5]),
-                              (int)pack2_out<DT_F16>(sc[t][8 * j + 6], sc[t][8 * j + 7])};
-      }
-      l += sum;
-      int down = (lh ? v1 : v0) - bmax;
-      down = down < -126 ? -126 : down;
-      const float vscale = __builtin_ldexpf(1.0f, down);
-      __builtin_amdgcn_sched_barrier(0);
-      const uint8_t* const vr = st + kTileBytes + lr * 64;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        v4i x[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) x[t] = *(const v4i*)(vr + n * 2048 + (((2 * lh + t) ^ val_swz(lr)) << 4));
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          acc[n] = mma32<DT_F16>(widen8<DT_F16>(x[t][0], x[t][1], vscale), pf[2 * t], acc[n]);
-          acc[n] = mma32<DT_F16>(widen8<DT_F16>(x[t][2], x[t][3], vscale), pf[2 * t + 1], acc[n]);
-        }
+    // chunk j of this thread: codes tid + j threads, the keys' (of step ik) first, then the values' (of iv)
+    v4i code[kPer];
+    auto is_key = [&](int j) {
+      return (j + 1) * kThr <= kChunks ? true : j * kThr >= kChunks ? false : wave * 64 + j * kThr < kChunks;
+    };
+    // (a step past the run's last is read as the last, and never used)
+    auto load_one = [&](auto J, int ik, int iv, int n, int kb_run) {
+      constexpr int j = decltype(J)::value;
+      const int c = tid + j * kThr;
+      if (is_key(j)) {
+        ik = ik < n ? ik : n - 1;
+        const int key = c / (D / 16), off = (kb_run + ik * kStep + key) & (kv.page - 1);
+        code[j] = *(const v4i*)(kv.k + s_page[2 * ik + (key >> 5)] + off * D + c % (D / 16) * 16);
+      } else {
+        iv = iv < n ? iv : n - 1;
+        const int f = (c - kChunks) / 4, kc = (c & 3) * 16, off = (kb_run + iv * kStep + kc) & (kv.page - 1);
+        code[j] = *(const v4i*)(kv.v + s_page[2 * iv + (kc >> 5)] + f * kv.page + off);
       }
     };
-    // Value codes of keys that no row sees are cleared in LDS (they may be anything, NaN codes
-    // included; their scores are masked).  Uniform over the workgroup.
-    auto clear = [&](int i, int kb) {
-      uint8_t* const st = smem + (i % kStages) * 2 * kTileBytes + kTileBytes;
-      for (int slot = tid; slot < D * 4; slot += kThreads) {
-        const int f = slot >> 2, key = kb + 16 * ((slot & 3) ^ val_swz(f));
-        v4i x = *(const v4i*)(st + slot * 16);
+    auto load = [&](int ik, int iv, int n, int kb_run) {
+      each<kPer>([&](auto J) { load_one(J, ik, iv, n, kb_run); });
+    };
+    // codes of keys that no row sees may be anything, NaN included: the values' are cleared (the scores
+    // are masked)
+    auto clear = [&](int iv, int kb_run) {
+      const int kb = kb_run + iv * kStep;
+      if (kb >= klo && kb + kStep <= khi) return;
+      const int first = kb + 16 * (tid & 3);
+      each<kPer>([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        if (is_key(j)) return;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t keep = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) keep |= key + 4 * w + e >= klo && key + 4 * w + e < khi ? 0xffu << (8 * e) : 0u;
-          x[w] &= (int)keep;
+          for (int e = 0; e < 4; ++e) {
+            const int key = first + 4 * w + e;
+            keep |= key >= klo && key < khi ? 0xffu << (8 * e) : 0u;
+          }
+          code[j][w] &= (int)keep;
         }
-        *(v4i*)(st + slot * 16) = x;
+      });
+    };
+    // A lane's two 16-byte writes go out in an order that gives every eight lanes eight different
+    // chunk numbers modulo 8 (a ds_write_b128 serves eight lanes a cycle over 32 banks).
+    auto put_one = [&](auto J, int ik, int iv) {
+      constexpr int j = decltype(J)::value;
+      const int x0 = code[j][0], x1 = code[j][1], x2 = code[j][2], x3 = code[j][3];
+      const int c = tid + j * kThr;
+      if (is_key(j)) {
+        const int row = c / (D / 16), src = c % (D / 16);
+        const int odd = D > 64 ? (src >> 2) & 1 : 0, swap = -odd;
+        uint8_t* const at = smem + (ik & 1) * kTileBytes + row * (2 * D);
+        const int place = ((2 * src + odd) ^ key_swz<D>(row)) << 4;
+        *(v4i*)(at + place) = widen8<DT>(pick(swap, x0, x2), pick(swap, x1, x3), 1.0f);
+        __builtin_amdgcn_sched_barrier(0);
+        *(v4i*)(at + (place ^ 16)) = widen8<DT>(pick(swap, x2, x0), pick(swap, x3, x1), 1.0f);
+      } else {
+        int down = (s_exp[(2 * iv + ((tid & 3) >> 1)) & (kMeta - 1)] >> 8) - bmax;
+        down = down < -126 ? -126 : down;
+        const float vscale = __uint_as_float((uint32_t)(127 + down) << 23);
+        const int row = (c - kChunks) / 4, src = c & 3;
+        const int odd = row & 1, swap = -odd;
+        uint8_t* const at = smem + (2 + (iv & 1)) * kTileBytes + row * 128;
+        const int place = ((2 * src + odd) ^ val_swz(row)) << 4;
+        *(v4i*)(at + place) = widen8<DT_F16>(pick(swap, x0, x2), pick(swap, x1, x3), vscale);
+        __builtin_amdgcn_sched_barrier(0);
+        *(v4i*)(at + (place ^ 16)) = widen8<DT_F16>(pick(swap, x2, x0), pick(swap, x3, x1), vscale);
       }
-      __syncthreads();
+    };
+    auto put = [&](int ik, int iv) {
+      each<kPer>([&](auto J) { put_one(J, ik, iv); });
+    };
+
+    // operand row of key tile T: LDS key 32 h' + 16 T + 4 a + b of row 8 a + 4 h' + b
+    const int key0 = 32 * ((lr >> 2) & 1) + 4 * (lr >> 3) + (lr & 3);
+    const int krow = key0 * (2 * D), kz = key_swz<D>(key0);
+    static_assert(key_swz<D>(16) == 0, "both key tiles swizzle alike");
+    auto key_op = [&](int i, int x) {              // MFMA x of the scores: key tile x % 2, features x / 2
+      return *(const v4i*)(smem + (i & 1) * kTileBytes + krow + (x & 1) * 32 * D + (((lh * KS + (x >> 1)) ^ kz) << 4));
+    };
+    auto val_op = [&](int i, int x) {              // MFMA x of the output: features x % NT, keys x / NT
+      return *(const v4i*)(smem + (2 + (i & 1)) * kTileBytes + (x % NT) * 4096 + lr * 128 +
+                           (((4 * lh + x / NT) ^ val_swz(lr)) << 4));
+    };
+    v16 sc[2], sn[2];
+    v4i pf[4];
+    float kscale = 0.0f;
+    auto scores = [&](int i) {
+      sn[0] = v16{};
+      sn[1] = v16{};
+#pragma unroll
+      for (int x = 0; x < 2 * KS; ++x) {
+        sn[x & 1] = mma32<DT>(key_op(i, x), qf[x >> 1], sn[x & 1]);
+        if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto highest = [&] {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sn[t][r]);
+      return mx;
+    };
+    // the scores of step i (largest: mx) become the current ones
+    auto settle = [&](int i, int kb, float mx) {
+      if (!(kb >= all_lo && kb + kStep <= all_hi)) {
+        // register 16 t + r is key kb + 32 h + 16 t + r: the row sees those from `low` to below `high`
+        const int high = (a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total) - kb - 32 * lh;
+        const int low = (a.window > 0 ? pos - a.window + 1 : 0) - kb - 32 * lh;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sn[t][r] = 16 * t + r >= low && 16 * t + r < high ? sn[t][r] : -INFINITY;
+        mx = highest();
+      }
+      // not 0: a masked score of -inf stays one
+      kscale = fmaxf(exp_byte(s_exp[2 * i + lh] & 255) * scale, 1.17549435e-38f);
+      mx *= kscale;
+      if (__any(mx > m + 8.0f)) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float mn = fmaxf(m, mx);
+        const float alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        m = mn;
+        l *= alpha;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] *= alpha;
+      }
+      sc[0] = sn[0];
+      sc[1] = sn[1];
+    };
+    // this wave's LDS accesses are done, then everybody's (the loads of codes stay in flight)
+    auto meet = [&] {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
     };
 
     for (int run = 0; run < steps; run += kMeta / 2) {
       const int n = steps - run < kMeta / 2 ? steps - run : kMeta / 2;
       const int kb_run = kb0 + run * kStep;
-      {
+      __syncthreads();                           // the run before is read
+      int top = 0;
+      if (tid < kMeta) {
         // a half that no row sees reads page 0 and counts as values of exponent 0
         const int key = kb_run + 32 * tid;
         const bool seen = key < khi && key + 32 > klo;
         int p = seen ? kv.table[(int64_t)s * kv.max_pages + key / kv.page] : 0;
         p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
         p = p * kv.kv_heads + head;
-        s_page[tid] = p;
-        s_exp[tid] = kv.ke[p] | (seen ? kv.ve[p] << 8 : 0);
+        s_page[tid] = (int64_t)p * (kv.page * D);
+        top = seen && tid < 2 * n ? kv.ve[p] : 0;
+        s_exp[tid] = kv.ke[p] | top << 8;
       }
+      // values enter the product relative to the largest exponent so far
+      const float wtop = wave_max((float)top);
+      if (lane == 0) s_top[wave] = (int)wtop;
       __syncthreads();
+      int bn = bmax;
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) dma(i, n, kb_run);
-      for (int i = 0; i < n; ++i) {
-        // step i is this wave's oldest stage in LDS; two later ones may be on their way (past the last
-        // step the DMA repeats it, so that the count is always the same)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 2) * 2 * kLoads) : "memory");
-        __builtin_amdgcn_s_barrier();              // and every wave is past step i - 1
-        asm volatile("" ::: "memory");
-        dma(i + kStages - 1, n, kb_run);
-        const int kb = kb_run + i * kStep;
-        if (kb < klo || kb + kStep > khi) clear(i, kb);
-        step(i, kb);
-        __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
+      for (int w = 0; w < NW; ++w) bn = s_top[w] > bn ? s_top[w] : bn;
+      if (bn > bmax && run > 0) {
+        const float fix = __builtin_ldexpf(1.0f, bmax - bn < -126 ? -126 : bmax - bn);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] *= fix;
       }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
+      bmax = bn;
+      // Step i multiplies the next step's scores beside its own softmax and puts the codes of the steps
+      // after into the buffers that step i - 1 has left.
+      load(0, 0, n, kb_run);
+      put(0, 0);
+      load(1, 0, n, kb_run);
+      clear(0, kb_run);
+      put(1, 0);
+      meet();
+      scores(0);
+      settle(0, kb_run, highest());
+      load(2, 1, n, kb_run);
+      meet();
+      for (int i = 0; i < n; ++i) {
+        const int next = i + 1 < n ? i + 1 : n - 1;
+        clear(next, kb_run);
+        // Slot x: one MFMA of the next scores, the read of the operand four MFMAs on, and a share of the
+        // softmax; then one MFMA of the output, a read, and a share of the search for the next maximum.
+        // The order is pinned: left to itself the compiler moves the softmax away from the MFMAs and
+        // waits for every read in front of its MFMA.
+        constexpr int kAheadOps = 4, kKeyOps = 2 * KS, kValOps = 4 * NT;
+        constexpr int kShare = 32 / kKeyOps, kSeek = 32 / kValOps;
+        static_assert(kKeyOps % kAheadOps == 0, "the ring of operands runs on from the keys' to the values'");
+        const float ref = m == -INFINITY ? 0.0f : m;
+        v4i op[kAheadOps];
+#pragma unroll
+        for (int x = 0; x < kAheadOps; ++x) op[x] = key_op(i + 1, x);
+        sn[0] = v16{};
+        sn[1] = v16{};
+        float sum = 0.0f, mx = -INFINITY;
+        __builtin_amdgcn_sched_barrier(0);
+        each<kKeyOps>([&](auto X) {
+          constexpr int x = decltype(X)::value;
+          sn[x & 1] = mma32<DT>(op[x % kAheadOps], qf[x >> 1], sn[x & 1]);
+          op[x % kAheadOps] = x + kAheadOps < kKeyOps ? key_op(i + 1, x + kAheadOps) : val_op(i, x + kAheadOps - kKeyOps);
+#pragma unroll
+          for (int e = x * kShare; e < (x + 1) * kShare; ++e) {
+            const int t = e >> 4, r = e & 15;
+            sc[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], kscale, -ref));
+            sum += sc[t][r];
+            if ((e & 7) == 7)
+              pf[e >> 3] = v4i{(int)pack2_out<DT_F16>(sc[t][r - 7], sc[t][r - 6]), (int)pack2_out<DT_F16>(sc[t][r - 5], sc[t][r - 4]),
+                               (int)pack2_out<DT_F16>(sc[t][r - 3], sc[t][r - 2]), (int)pack2_out<DT_F16>(sc[t][r - 1], sc[t][r])};
+          }
+          asm volatile("" : "+v"(sum));
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        l += sum;
+        each<kValOps>([&](auto X) {
+          constexpr int x = decltype(X)::value;
+          acc[x % NT] = mma32<DT_F16>(op[x % kAheadOps], pf[x / NT], acc[x % NT]);
+          if constexpr (x + kAheadOps < kValOps) op[x % kAheadOps] = val_op(i, x + kAheadOps);
+#pragma unroll
+          for (int e = x * kSeek; e < (x + 1) * kSeek; ++e) mx = fmaxf(mx, sn[e >> 4][e & 15]);
+          asm volatile("" : "+v"(mx));
+          __builtin_amdgcn_sched_barrier(0);
+          // the codes that have arrived into LDS, the next ones requested, spread over the slots
+          each<kPer>([&](auto J) {
+            if constexpr (x == (decltype(J)::value + 1) * kValOps / (kPer + 2)) {
+              put_one(J, i + 2, i + 1);
+              __builtin_amdgcn_sched_barrier(0);
+              load_one(J, i + 3, i + 2, n, kb_run);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          });
+        });
+        settle(next, kb_run + next * kStep, mx);
+        meet();
+      }
     }
 
     l += __shfl_xor(l, 32);
-    if (row < rows) {
+    // the lane's row again (its place in the output need not live through the loop)
+    int again = lane & 31;
+    asm volatile("" : "+v"(again));
+    const int orw = r0 + 32 * wave + again;
+    if (orw < rows) {
       const float vtrue = exp_byte(bmax);
-      const int64_t orow = (int64_t)(sp.first + tok) * a.heads + head * group + hq;
+      const int otok = orw / group;
+      const int64_t orow = (int64_t)(sp.first + otok) * a.heads + head * group + (orw - otok * group);
       const float inv = (splits > 1 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f)) * vtrue;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -640,7 +727,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks,
   }
 }
 
-constexpr int kSmallRows = 16;      // up to here one 16-row tile, above 128-row blocks
+constexpr int kSmallRows = 16;      // up to here one 16-row tile
 
 // How a call is cut: rows of one workgroup, row blocks of a sequence, splits of the keys and keys of
 // one split.
@@ -648,15 +735,20 @@ struct Plan {
   int64_t per, blocks;
   int splits, chunk;
 };
-Plan plan_of(int64_t rows, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
+Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
   Plan p;
-  p.per = rows > kSmallRows ? kBlockRows : kSmallRows;
+  const int64_t pairs = (int64_t)seqs * kv_heads;
+  // Many rows: 8 waves (two on a SIMD) share a step's codes; 4 at 256 features, whose accumulators,
+  // queries and scores fit a wave only where it has the SIMD's registers to itself, and at 64 features
+  // where blocks of 256 rows would leave CUs without one.
+  p.per = rows <= kSmallRows ? kSmallRows
+          : dim == 256 || (dim == 64 && pairs * ((rows + 255) / 256) < 256) ? 128 : 256;
   p.blocks = (rows + p.per - 1) / p.per;
   int64_t keys = max_kv;
   if (window > 0 && window + max_q + kTile < keys) keys = window + max_q + kTile;
-  const int64_t groups = (int64_t)seqs * kv_heads * p.blocks;
+  const int64_t groups = pairs * p.blocks;
   const int64_t step = kWaves * kTile;
-  int64_t want = (1024 + groups - 1) / groups;
+  int64_t want = p.per == kSmallRows ? (1024 + groups - 1) / groups : groups >= 192 ? 1 : 512 / groups;
   const int64_t most = (keys + step - 1) / step;
   want = want > most ? most : want;
   want = want < 1 ? 1 : want;
@@ -665,7 +757,7 @@ Plan plan_of(int64_t rows, int kv_heads, int seqs, int64_t max_q, int64_t max_kv
   p.splits = (int)((keys + c - 1) / c);
   if (p.splits < 1) p.splits = 1;
   p.chunk = (int)c;
-  const int64_t most_blocks = ((int64_t)1 << 30) / ((int64_t)seqs * kv_heads * p.splits);
+  const int64_t most_blocks = ((int64_t)1 << 30) / (pairs * p.splits);
   if (p.per == kSmallRows && p.blocks > 65535 / seqs) p.blocks = 65535 / seqs;
   if (p.blocks > most_blocks) p.blocks = most_blocks;
   if (p.blocks < 1) p.blocks = 1;
@@ -675,20 +767,24 @@ Plan plan_of(int64_t rows, int kv_heads, int seqs, int64_t max_q, int64_t max_kv
 template <int D, int DT>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.heads / a.kv.kv_heads);
-  const Plan p = plan_of(rows, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
+  const Plan p = plan_of(rows, D, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
+  const int blocks = (int)p.blocks;
   if (p.per == kSmallRows) {
     const dim3 grid((unsigned)p.splits, (unsigned)a.kv.kv_heads, (unsigned)(p.blocks * a.kv.seqs));
-    k_attn_rows<D, 1, DT><<<grid, kThreads, 0, st>>>(a, (int)p.blocks, p.chunk);
+    k_attn_rows<D, 1, DT><<<grid, kThreads, 0, st>>>(a, blocks, p.chunk);
   } else {
     const unsigned grid = (unsigned)(p.blocks * a.kv.seqs * a.kv.kv_heads * p.splits);
-    k_attn_tiles<D, DT><<<grid, kThreads, 0, st>>>(a, (int)p.blocks, p.splits, p.chunk);
+    if constexpr (D != 128)
+      if (p.per == 128) k_attn_tiles<D, DT, 4><<<grid, 256, 0, st>>>(a, blocks, p.splits, p.chunk);
+    if constexpr (D != 256)
+      if (p.per == 256) k_attn_tiles<D, DT, 8><<<grid, 512, 0, st>>>(a, blocks, p.splits, p.chunk);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  int64_t blocks = ((int64_t)a.max_q * a.heads + 3) / 4;
+  int64_t jb = ((int64_t)a.max_q * a.heads + 3) / 4;
   const int64_t limit = ((int64_t)1 << 30) / a.kv.seqs;
-  blocks = blocks > limit ? limit : blocks;
-  k_attn_join<D, DT><<<(unsigned)(blocks * a.kv.seqs), 256, 0, st>>>(a, (int)blocks, p.splits);
+  jb = jb > limit ? limit : jb;
+  k_attn_join<D, DT><<<(unsigned)(jb * a.kv.seqs), 256, 0, st>>>(a, (int)jb, p.splits);
   return hipGetLastError();
 }
 template <int DT>
@@ -702,9 +798,8 @@ hipError_t launch_dt(const AttnArgs& a, int dim, hipStream_t st) {
 
 }  // namespace
 
-int attn_splits(int64_t tokens, int heads, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
-  (void)tokens;
-  return plan_of(max_q * (heads / kv_heads), kv_heads, seqs, max_q, max_kv, window).splits;
+int attn_splits(int heads, int kv_heads, int dim, int seqs, int64_t max_q, int64_t max_kv, int window) {
+  return plan_of(max_q * (heads / kv_heads), dim, kv_heads, seqs, max_q, max_kv, window).splits;
 }
 
 hipError_t launch_attention(const AttnArgs& a, int dt, int dim, hipStream_t st) {

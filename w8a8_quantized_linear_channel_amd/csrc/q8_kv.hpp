@@ -45,7 +45,7 @@ struct AttnArgs {
   float *part, *part_ml;           // [splits, tokens * heads, dim], [splits, tokens * heads, 2]
 };
 // Splits of the key axis for this shape (1: no workspace, one launch).
-int attn_splits(int64_t tokens, int heads, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window);
+int attn_splits(int heads, int kv_heads, int dim, int seqs, int64_t max_q, int64_t max_kv, int window);
 hipError_t launch_attention(const AttnArgs& a, int dt, int dim, hipStream_t st);
 
 // Block-scaled FP8 (fp8_block.hip): activations [M, K] in groups of 128 along
