@@ -467,9 +467,10 @@ q8_status q8_gemm_fp8_block(const uint8_t* xq, const float* x_scale, int64_t M, 
                             void* y, q8_dtype y_dtype, void* stream);
 
 /*
- * q8_linear_fp8_block -- q8_quantize_act_block followed by q8_gemm_fp8_block.
+ * q8_linear_fp8_block -- q8_quantize_act_block followed by q8_gemm_fp8_block;
+ * for M <= 4 in one launch, the codes passing through LDS.
  * x: [M, K] of x_dtype (F32, F16, BF16); y of y_dtype (F16 or BF16).
- * workspace: q8_workspace_bytes(Q8_OP_FP8_BLOCK, M, N, K).
+ * workspace: q8_workspace_bytes(Q8_OP_FP8_BLOCK, M, N, K) bytes (0 for M <= 4).
  */
 q8_status q8_linear_fp8_block(const void* x, q8_dtype x_dtype, int64_t M, int64_t K,
                               const uint8_t* wq, const float* w_scale, int64_t N,

@@ -151,8 +151,9 @@ Fp8Ws fp8_ws(int64_t M, int64_t K) {
 
 // Block-scaled FP8: codes and the scales [ceil(K / 128), M].
 Fp8Ws fp8_block_ws(int64_t M, int64_t K) {
+  Fp8Ws w{0, 0, 0};
+  if (q8::fp8_block_is_fused(M)) return w;      // the codes stay in LDS
   Carve c;
-  Fp8Ws w;
   w.xq = c.take((size_t)M * K);
   w.xs = c.take((size_t)M * ((K + q8::kScaleBlock - 1) / q8::kScaleBlock) * 4);
   w.total = c.off;
@@ -814,6 +815,8 @@ q8_status q8_linear_fp8_block(const void* x, q8_dtype x_dtype, int64_t M, int64_
   Q8_TRY(check_device(st));
   Q8_TRY(check_ptrs(st, {x, wq, w_scale, bias, y, ws.total > 0 ? workspace : nullptr}));
   if (M == 0) return Q8_OK;
+  if (q8::fp8_block_is_fused(M))
+    return launched(q8::launch_gemv_fp8_block(x, x_dtype, M, K, wq, w_scale, N, bias, y, y_dtype, st));
   char* base = static_cast<char*>(workspace);
   uint8_t* xq = reinterpret_cast<uint8_t*>(base + ws.xq);
   float* xs = reinterpret_cast<float*>(base + ws.xs);

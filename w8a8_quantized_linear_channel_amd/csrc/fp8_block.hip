@@ -379,92 +379,226 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
 }
 
 // ---------------------------------------------------------------- few tokens
-// Decode-shaped: a workgroup owns 16 weight rows, its 4 waves take every
+// Decode-shaped: a workgroup owns 16 NF weight rows, its 4 waves take every
 // fourth block of K (v_mfma_f32_16x16x128_f8f6f4: one block an instruction),
-// up to kAhead blocks' weights requested ahead, straight into registers, and
-// join through LDS.  MF fragments of 16 tokens share a weight operand.
-constexpr int kAhead = 8;
-template <int MF, int YDT>
+// AHEAD blocks at a time, all of whose weights and activations are requested
+// before the first is used, straight into registers, and join through LDS.  MF
+// fragments of 16 tokens share a weight operand, NF fragments of 16 weight rows
+// an activation operand.
+constexpr int kGemvWaves = kThreads / 64;
+
+// Joins the waves' sums of a 16 NF x 16 MF tile and stores them.
+template <int MF, int NF, int YDT>
+__device__ __forceinline__ void gemv_store(v4f (&acc)[NF][MF], v4f (*part)[NF * MF][64], int wave, int lane, int M, int N,
+                                           int n0, const float* bias, void* y) {
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) part[wave][i * MF + f][lane] = acc[i][f];
+  __syncthreads();
+  const int lr = lane & 15, lg = lane >> 4;
+  for (int q = wave; q < NF * MF; q += kGemvWaves) {
+    const int m = 16 * (q % MF) + lr, n4 = n0 + 16 * (q / MF) + 4 * lg;
+    if (m >= M) continue;
+    v4f t = part[0][q][lane];
+#pragma unroll
+    for (int w = 1; w < kGemvWaves; ++w) t += part[w][q][lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n4 + r < N) store_out<YDT>(y, (int64_t)m * N + n4 + r, t[r] + (bias ? bias[n4 + r] : 0.0f));
+  }
+}
+
+__device__ __forceinline__ v8i join8(const v4i a, const v4i b) {
+  return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+template <int MF, int NF, int AHEAD, int YDT>
 __global__ __launch_bounds__(kThreads) void k_gemv_block(const uint8_t* __restrict__ xq, const float* __restrict__ x_scale,
                                                          int M, int K, const uint8_t* __restrict__ wq,
                                                          const float* __restrict__ w_scale, int N,
                                                          const float* __restrict__ bias, void* __restrict__ y) {
-  constexpr int kWaves = kThreads / 64;
-  __shared__ v4f part[kWaves][MF][64];
+  __shared__ v4f part[kGemvWaves][NF * MF][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int n0 = blockIdx.x * 16 * NF;
+  const int groups = (K + kScaleBlock - 1) / kScaleBlock;
+  // rows past N and tokens past M read the last ones and are not stored
+  const uint8_t *wp[NF], *xp[MF];
+  const float *ws[NF], *xs[MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    const int n = n0 + 16 * i + lr < N ? n0 + 16 * i + lr : N - 1;
+    wp[i] = wq + (int64_t)n * K + 32 * lg;
+    ws[i] = w_scale + (int64_t)(n / kScaleBlock) * groups;
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int m = 16 * f + lr < M ? 16 * f + lr : M - 1;
+    xp[f] = xq + (int64_t)m * K + 32 * lg;
+    xs[f] = x_scale + m;
+  }
+  v4f acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) acc[i][f] = v4f{0, 0, 0, 0};
+  const int whole = K / kScaleBlock;
+  for (int j0 = wave; j0 < groups; j0 += kGemvWaves * AHEAD) {
+    v4i w[AHEAD][NF][2], x[AHEAD][MF][2];
+    float sx[AHEAD][MF], sw[AHEAD];
+    const int live = j0 + (AHEAD - 1) * kGemvWaves < whole ? AHEAD : 0;      // all blocks whole: no checks
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int j = j0 + u * kGemvWaves, jc = j < groups ? j : groups - 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = jc * kScaleBlock + 16 * h;
+        const bool in = live || (j < groups && k + 32 * lg < K);
+#pragma unroll
+        for (int f = 0; f < MF; ++f) x[u][f][h] = in ? *(const v4i*)(xp[f] + k) : v4i{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int f = 0; f < MF; ++f) sx[u][f] = xs[f][(int64_t)jc * M];
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int j = j0 + u * kGemvWaves, jc = j < groups ? j : groups - 1;
+      sw[u] = ws[0][jc];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = jc * kScaleBlock + 16 * h;
+        const bool in = live || (j < groups && k + 32 * lg < K);
+#pragma unroll
+        for (int i = 0; i < NF; ++i) w[u][i][h] = in ? *(const v4i*)(wp[i] + k) : v4i{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const float sc = sw[u] * sx[u][f];
+        const v8i xv = join8(x[u][f][0], x[u][f][1]);
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join8(w[u][i][0], w[u][i][1]), xv, v4f{0, 0, 0, 0}, 0,
+                                                                        0, 0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][f][r] = __builtin_fmaf(sc, p[r], acc[i][f][r]);
+        }
+      }
+  }
+  gemv_store<MF, NF, YDT>(acc, part, wave, lane, M, N, n0, bias, y);
+}
+
+// Up to kFusedM tokens: the activations are quantized on the way, each wave
+// its own blocks of K (16 consecutive features a lane, a block's maximum over 8
+// lanes), through LDS into MFMA operands, while its weights are on their way:
+// one launch and no workspace.
+constexpr int kFusedM = 4;
+template <int XDT, int YDT>
+__global__ __launch_bounds__(kThreads) void k_gemv_block_fused(const void* __restrict__ x, int M, int K,
+                                                               const uint8_t* __restrict__ wq,
+                                                               const float* __restrict__ w_scale, int N,
+                                                               const float* __restrict__ bias, void* __restrict__ y) {
+  constexpr int AHEAD = 8;
+  static_assert(AHEAD * 8 == 64, "a wave's lanes hold its blocks, 8 lanes a block");
+  __shared__ v4f part[kGemvWaves][1][64];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kGemvWaves][kFusedM][AHEAD * kScaleBlock];
+  __shared__ float scales[kGemvWaves][kFusedM][AHEAD];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int n0 = blockIdx.x * 16;
   const int groups = (K + kScaleBlock - 1) / kScaleBlock;
-  const uint8_t* const wp = wq + (int64_t)(n0 + lr < N ? n0 + lr : N - 1) * K;
+  const int n = n0 + lr < N ? n0 + lr : N - 1;
+  const uint8_t* const wp = wq + (int64_t)n * K + 32 * lg;
   const float* const ws = w_scale + (int64_t)(n0 / kScaleBlock) * groups;
-  int xr[MF];
+  const int mr = lr < M ? lr : M - 1;
+  v4f acc[1][1] = {{v4f{0, 0, 0, 0}}};
+  for (int j0 = wave; j0 < groups; j0 += kGemvWaves * AHEAD) {
+    // this lane's 16 features, of block lane / 8
+    const int kx = (j0 + (lane >> 3) * kGemvWaves) * kScaleBlock + 16 * (lane & 7);
+    const bool inx = kx < K;
+    constexpr int kPieces = XDT == DT_F32 ? 4 : 2;
+    v4i raw[kFusedM][kPieces];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) xr[f] = 16 * f + lr < M ? 16 * f + lr : M - 1;
-  v4f acc[MF];
+    for (int m = 0; m < kFusedM; ++m)
+      if (m < M) {
+        const v4i* p = (const v4i*)((const char*)x + ((int64_t)m * K + (inx ? kx : 0)) * (XDT == DT_F32 ? 4 : 2));
 #pragma unroll
-  for (int f = 0; f < MF; ++f) acc[f] = v4f{0, 0, 0, 0};
-  // both halves of the lane's 32 bytes of block j; bytes past K are zeros
-  auto load = [&](const uint8_t* p, int j, v4i* o) {
+        for (int c = 0; c < kPieces; ++c) raw[m][c] = p[c];
+      }
+    v4i w[AHEAD][2];
+    float sw[AHEAD];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = j * kScaleBlock + 32 * lg + 16 * h;
-      const v4i v = *(const v4i*)(p + (k < K ? k : 0));
-      o[h] = k < K ? v : v4i{0, 0, 0, 0};
-    }
-  };
-  for (int j0 = wave; j0 < groups; j0 += kWaves * kAhead) {
-    v4i w[kAhead][2];
-    float s[kAhead];
+    for (int u = 0; u < AHEAD; ++u) {
+      const int j = j0 + u * kGemvWaves, jc = j < groups ? j : groups - 1;
+      sw[u] = ws[jc];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int j = j0 + u * kWaves < groups ? j0 + u * kWaves : j0;
-      load(wp, j, w[u]);
-      s[u] = ws[j];
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int j = j0 + u * kWaves;
-      if (j < groups) {
-        const v8i a = {w[u][0][0], w[u][0][1], w[u][0][2], w[u][0][3], w[u][1][0], w[u][1][1], w[u][1][2], w[u][1][3]};
-#pragma unroll
-        for (int f = 0; f < MF; ++f) {
-          v4i x[2];
-          load(xq + (int64_t)xr[f] * K, j, x);
-          const v8i b = {x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
-          const float sc = s[u] * x_scale[(int64_t)j * M + xr[f]];
-          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[f][r] = __builtin_fmaf(sc, p[r], acc[f][r]);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int k = jc * kScaleBlock + 16 * h;
+        w[u][h] = *(const v4i*)(wp + (k + 32 * lg < K ? k : -32 * lg));
       }
     }
-  }
 #pragma unroll
-  for (int f = 0; f < MF; ++f) part[wave][f][lane] = acc[f];
-  __syncthreads();
-  for (int f = wave; f < MF; f += kWaves) {
-    const int m = 16 * f + lr;
-    if (m >= M) continue;
-    v4f t = part[0][f][lane];
+    for (int m = 0; m < kFusedM; ++m)
+      if (m < M) {
+        float v[16];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) t += part[w][f][lane];
+        for (int c = 0; c < kPieces; ++c) Chunk<XDT>::decode(raw[m][c], v + c * Chunk<XDT>::kElems);
+        float amax = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int n = n0 + 4 * lg + r;
-      if (n < N) store_out<YDT>(y, (int64_t)m * N + n, t[r] + (bias ? bias[n] : 0.0f));
+        for (int e = 0; e < 16; ++e) {
+          v[e] = inx ? v[e] : 0.0f;
+          amax = fmaxf(amax, fabsf(v[e]));
+        }
+        // over the block's 8 lanes: pairs, pairs of pairs, the half-row's two quads
+        int am = __float_as_int(amax);
+        auto up = [](int a, int b) { return a > b ? a : b; };     // of non-negative floats
+        am = up(am, __builtin_amdgcn_update_dpp(0, am, 0xB1, 0xF, 0xF, false));
+        am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x4E, 0xF, 0xF, false));
+        am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x141, 0xF, 0xF, false));
+        float s = __int_as_float(am) / kFp8Max;
+        s = s < kEps ? kEps : s;
+        const v2i lo = codes8<XDT>(v, s), hi = codes8<XDT>(v + 8, s);
+        *(v4i*)&codes[wave][m][lane * 16] = v4i{lo[0], lo[1], hi[0], hi[1]};
+        if ((lane & 7) == 0) scales[wave][m][lane >> 3] = s;
+      }
+    // (LDS of this wave only, which it reads after its own writes)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      // codes past K are zeros, so the weights there (of the row's start) add nothing
+      const v4i* c = (const v4i*)&codes[wave][mr][u * kScaleBlock + 32 * lg];
+      const float sc = sw[u] * scales[wave][mr][u];
+      const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join8(w[u][0], w[u][1]), join8(c[0], c[1]),
+                                                                     v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[0][0][r] = __builtin_fmaf(sc, p[r], acc[0][0][r]);
     }
   }
+  gemv_store<1, 1, YDT>(acc, part, wave, lane, M, N, n0, bias, y);
 }
 
 template <int YDT>
 hipError_t launch_product(const uint8_t* xq, const float* xs, int M, int K, const uint8_t* wq, const float* ws, int N,
                           const float* bias, void* y, hipStream_t st) {
   if (M <= 64) {
-    const unsigned grid = (unsigned)((N + 15) / 16);
-    if (M <= 16) k_gemv_block<1, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-    else if (M <= 32) k_gemv_block<2, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-    else k_gemv_block<4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    // 32 weight rows a workgroup halve the activation reads where that still gives every CU two of them
+    const bool wide = N >= 32 * 512;
+    const unsigned grid = (unsigned)((N + (wide ? 31 : 15)) / (wide ? 32 : 16));
+    if (M <= 16) {
+      if (wide) k_gemv_block<1, 2, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+      else k_gemv_block<1, 1, 8, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    } else if (M <= 32) {
+      if (wide) k_gemv_block<2, 2, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+      else k_gemv_block<2, 1, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    } else {
+      if (wide) k_gemv_block<4, 2, 2, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+      else k_gemv_block<4, 1, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    }
     return hipGetLastError();
   }
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
@@ -506,6 +640,28 @@ hipError_t launch_gemm_fp8_block(const uint8_t* xq, const float* x_scale, int64_
                                  const float* w_scale, int64_t N, const float* bias, void* y, int ydt, hipStream_t st) {
   if (ydt == DT_F16) return launch_product<DT_F16>(xq, x_scale, (int)M, (int)K, wq, w_scale, (int)N, bias, y, st);
   return launch_product<DT_BF16>(xq, x_scale, (int)M, (int)K, wq, w_scale, (int)N, bias, y, st);
+}
+
+namespace {
+template <int XDT>
+hipError_t launch_fused(const void* x, int M, int K, const uint8_t* wq, const float* ws, int N, const float* bias, void* y,
+                        int ydt, hipStream_t st) {
+  const unsigned grid = (unsigned)((N + 15) / 16);
+  if (ydt == DT_F16) k_gemv_block_fused<XDT, DT_F16><<<grid, kThreads, 0, st>>>(x, M, K, wq, ws, N, bias, y);
+  else k_gemv_block_fused<XDT, DT_BF16><<<grid, kThreads, 0, st>>>(x, M, K, wq, ws, N, bias, y);
+  return hipGetLastError();
+}
+}  // namespace
+
+bool fp8_block_is_fused(int64_t M) { return M <= kFusedM; }
+
+hipError_t launch_gemv_fp8_block(const void* x, int xdt, int64_t M, int64_t K, const uint8_t* wq, const float* w_scale,
+                                 int64_t N, const float* bias, void* y, int ydt, hipStream_t st) {
+  switch (xdt) {
+    case DT_F32: return launch_fused<DT_F32>(x, (int)M, (int)K, wq, w_scale, (int)N, bias, y, ydt, st);
+    case DT_F16: return launch_fused<DT_F16>(x, (int)M, (int)K, wq, w_scale, (int)N, bias, y, ydt, st);
+    default: return launch_fused<DT_BF16>(x, (int)M, (int)K, wq, w_scale, (int)N, bias, y, ydt, st);
+  }
 }
 
 }  // namespace q8

@@ -753,7 +753,7 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
   want = want > most ? most : want;
   want = want < 1 ? 1 : want;
   int64_t c = ((keys + want - 1) / want + step - 1) / step * step;
-  c = c < step ? step : c;
+  c = c < 2 * step ? 2 * step : c;     // a shorter share costs the join more than it saves
   p.splits = (int)((keys + c - 1) / c);
   if (p.splits < 1) p.splits = 1;
   p.chunk = (int)c;

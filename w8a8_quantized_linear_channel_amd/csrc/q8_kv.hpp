@@ -58,5 +58,10 @@ hipError_t launch_quant_act_block(const void* x, int dt, int64_t M, int64_t K, u
                                   hipStream_t st);
 hipError_t launch_gemm_fp8_block(const uint8_t* xq, const float* x_scale, int64_t M, int64_t K, const uint8_t* wq,
                                  const float* w_scale, int64_t N, const float* bias, void* y, int ydt, hipStream_t st);
+// Decode-shaped, with the activation quantization in the same launch, for the few tokens where
+// fp8_block_is_fused.
+bool fp8_block_is_fused(int64_t M);
+hipError_t launch_gemv_fp8_block(const void* x, int xdt, int64_t M, int64_t K, const uint8_t* wq, const float* w_scale,
+                                 int64_t N, const float* bias, void* y, int ydt, hipStream_t st);
 
 }  // namespace q8
