@@ -1,16 +1,18 @@
 // Attention of new queries over the paged 8-bit key/value cache.
 //
-// One workgroup takes 16 RT rows (query tokens x the query heads that share a
-// kv head) of one sequence and kv head and one share of the keys; its 4 waves
-// take 128-key tiles in turn and join at the end.  Each wave computes
+// Up to 16 rows (query tokens x the query heads that share a kv head): one
+// workgroup takes them with one sequence, kv head and share of the keys; its NW
+// waves take 64-key tiles in turn and join at the end.  Each wave computes
 // S^T = K Q^T with v_mfma_f32_16x16x32 (16 keys x 16 rows), so lane (q, g)
-// (q = lane % 16, g = lane / 16) holds scores of row q.  The keys of the eight
-// 16-key MFMA tiles are dealt so that lane group g ends up with the 32
-// consecutive keys 32 g .. 32 g + 31: tile t's row 4 g + i is key 32 g + 4 t + i.
+// (q = lane % 16, g = lane / 16) holds scores of row q.  The keys of the four
+// 16-key MFMA tiles are dealt so that lane group g ends up with the 16
+// consecutive keys 16 g .. 16 g + 15: tile t's row 4 g + i is key 16 g + 4 t + i.
 // These are already the B operand of O^T = V^T P^T (contraction over keys), so
-// P needs no exchange between lanes, and lane (d, g) of the A operand is 32
+// P needs no exchange between lanes, and lane (d, g) of the A operand is 16
 // consecutive bytes of a row of the value cache, whose tokens are innermost.
-// K and V go from memory to registers to MFMA without LDS.
+// K and V go from memory to registers to MFMA without LDS, a tile's 8 D + 8 D
+// bytes all requested before the first is used: this is bound by the cache's
+// bytes.
 //
 // e4m3 codes convert to bf16 / f16 exactly (4 significant bits).  The key
 // exponent of a page multiplies the scores (one factor per lane and tile: 32
@@ -29,9 +31,7 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 128;     // keys of one wave step
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 64;      // keys of one wave step
 
 template <int DT>
 __device__ __forceinline__ v4f mma16(const v4i a, const v4i b, const v4f c) {
@@ -82,9 +82,10 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int s) {
   return r;
 }
 
-template <int D, int RT, int DT>
-__global__ __launch_bounds__(kThreads) void k_attn_rows(const AttnArgs a, int row_tiles, int chunk) {
+template <int D, int DT, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const AttnArgs a, int row_tiles, int chunk) {
   constexpr int KS = D / 32;        // MFMA steps over the features
+  constexpr int KL = D / 64;        // 16-byte loads of a lane's share of a key
   constexpr int NT = D / 16;        // 16-feature tiles of the output
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -96,212 +97,231 @@ __global__ __launch_bounds__(kThreads) void k_attn_rows(const AttnArgs a, int ro
   const Span sp = span_of(a, s);
   const int rows = sp.n * group;
   const bool split_out = gridDim.x > 1;
+  const int page_log2 = 31 - __builtin_clz(kv.page);
 
-  __shared__ __attribute__((aligned(16))) float s_acc[kWaves][16][D + 4];
-  __shared__ float s_ml[kWaves][16][2];
+  __shared__ __attribute__((aligned(16))) float s_acc[NW][16][D + 4];
+  __shared__ float s_ml[NW][16][2];
 
-  for (int r0 = tile0 * 16 * RT; r0 < rows; r0 += row_tiles * 16 * RT) {
-    // the rows of this lane, one in each row tile, and the keys that they see: [low, high)
-    int low[RT], high[RT];
-    v4i qf[RT][KS];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = r0 + 16 * t + lr;
-      const int rc = row < rows ? row : rows - 1;
-      const int tok = rc / group, hq = rc - tok * group;
-      const int pos = sp.past + tok;
-      high[t] = a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total;
-      low[t] = a.window > 0 ? pos - a.window + 1 : 0;
-      if (row >= rows) high[t] = 0;
+  for (int r0 = tile0 * 16; r0 < rows; r0 += row_tiles * 16) {
+    // this lane's row and the keys that it sees: [low, high)
+    const int row = r0 + lr, rc = row < rows ? row : rows - 1;
+    const int tok = rc / group, hq = rc - tok * group;
+    const int pos = sp.past + tok;
+    int high = a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total;
+    const int low = a.window > 0 ? pos - a.window + 1 : 0;
+    if (row >= rows) high = 0;
+    // features 64 i + 16 g .. + 15 of the row, as the lane's loads of a key give them
+    v4i qf[KS];
+    {
       const uint16_t* q = (const uint16_t*)a.q + (int64_t)(sp.first + tok) * a.q_stride +
-                          (int64_t)(head * group + hq) * D + lg * (D / 4);
+                          (int64_t)(head * group + hq) * D + 16 * lg;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) qf[t][ks] = *(const v4i*)(q + 8 * ks);
+      for (int ks = 0; ks < KS; ++ks) qf[ks] = *(const v4i*)(q + 64 * (ks >> 1) + 8 * (ks & 1));
     }
     // keys that any row of the tile sees
-    const int last = (r0 + 16 * RT < rows ? r0 + 16 * RT : rows) - 1;
+    const int last = (r0 + 16 < rows ? r0 + 16 : rows) - 1;
     const int pos0 = sp.past + r0 / group, pos1 = sp.past + last / group;
-    int klo = a.window > 0 && pos0 - a.window + 1 > 0 ? pos0 - a.window + 1 : 0;
-    int khi = a.causal ? (pos1 + 1 < sp.total ? pos1 + 1 : sp.total) : sp.total;
+    const int klo = a.window > 0 && pos0 - a.window + 1 > 0 ? pos0 - a.window + 1 : 0;
+    const int khi = a.causal ? (pos1 + 1 < sp.total ? pos1 + 1 : sp.total) : sp.total;
     // this workgroup's share: `chunk` keys from a multiple of kTile on, the last share all that is left
-    const int kb0 = (klo & ~(kTile - 1)) + (split * (int64_t)chunk < khi ? split * chunk : khi);
+    const int base = klo & ~(kTile - 1);
+    const int64_t from = (int64_t)split * chunk;
+    const int kb0 = base + from < khi ? base + (int)from : khi;
     const int kb1 = split + 1 < (int)gridDim.x && kb0 + (int64_t)chunk < khi ? kb0 + chunk : khi;
 
-    v4f acc[RT][NT];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      m[t] = -INFINITY;
-      l[t] = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[t][n] = v4f{0, 0, 0, 0};
-    }
+    v4f acc[NT];
+    float m = -INFINITY, l = 0.0f;
     int bmax = 0;          // the values' reference exponent byte
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
 
-    for (int kb = kb0 + wave * kTile; kb < kb1; kb += kWaves * kTile) {
-      // pages of the lane's K rows (chunk lr / 4) and of its own 32 keys (chunk lg);
-      // a chunk without a visible key reads page 0 and is masked
-      auto page_of = [&](int key) {
-        const int ok = key < khi && key + 32 > klo;
-        int p = ok ? kv.table[(int64_t)s * kv.max_pages + key / kv.page] : 0;
-        return p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
-      };
-      const int keyk = kb + 32 * (lr >> 2), keyv = kb + 32 * lg;
-      const int64_t ph_k = (int64_t)page_of(keyk) * kv.kv_heads + head;
-      const int64_t ph_v = (int64_t)page_of(keyv) * kv.kv_heads + head;
-      const uint8_t* kp = kv.k + (ph_k * kv.page + (keyk & (kv.page - 1)) + (lr & 3)) * D + lg * (D / 4);
-      const uint8_t* vp = kv.v + (ph_v * D + lr) * kv.page + (keyv & (kv.page - 1));
-      const float kscale = exp_byte(kv.ke[ph_v]) * a.scale_log2;
-      int vb = kv.ve[ph_v];
-      const bool seen = keyv < khi && keyv + 32 > klo;
-
-      v4f sc[RT][8];
+    // page of a 32-key half of a tile; one without a visible key reads page 0 and is masked
+    auto page_of = [&](int key) {
+      const bool ok = key < khi && key + 32 > klo;
+      int p = ok ? kv.table[(int64_t)s * kv.max_pages + (key >> page_log2)] : 0;
+      return p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
+    };
+    // A tile in registers.  The next one's is requested before the current one is used, and the pages of
+    // the one after that (of the lane's key rows, pk, and of its own 16 keys, pv) beside it.
+    struct Tile {
+      v4i k[4][KL], v[NT];
+      int ke, ve;
+    };
+    constexpr int kStride = NW * kTile;
+    int pk = 0, pv = 0;
+    auto pages = [&](int kb) {
+      if (kb >= kb1) return;
+      pk = page_of(kb + 32 * (lr >> 3));
+      pv = page_of(kb + 32 * (lg >> 1));
+    };
+    auto request = [&](Tile& x, int kb) {
+      if (kb >= kb1) return;
+      const int keyk = kb + 16 * (lr >> 2), keyv = kb + 16 * lg;
+      const int64_t ph_k = (int64_t)pk * kv.kv_heads + head, ph_v = (int64_t)pv * kv.kv_heads + head;
+      const uint8_t* const kp = kv.k + (ph_k * kv.page + (keyk & (kv.page - 1)) + (lr & 3)) * D + 16 * lg;
+      const uint8_t* const vp = kv.v + (ph_v * D + lr) * kv.page + (keyv & (kv.page - 1));
+      pages(kb + kStride);
 #pragma unroll
-      for (int t8 = 0; t8 < 8; ++t8) {
-        int kc[D / 16];
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const v4i x = *(const v4i*)(kp + (int64_t)t8 * 4 * D + 16 * i);
-          kc[4 * i] = x[0]; kc[4 * i + 1] = x[1]; kc[4 * i + 2] = x[2]; kc[4 * i + 3] = x[3];
-        }
+        for (int i = 0; i < KL; ++i) x.k[t][i] = *(const v4i*)(kp + t * 4 * D + 64 * i);
+      x.ke = kv.ke[ph_v];
+      x.ve = kv.ve[ph_v];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) sc[t][t8] = v4f{0, 0, 0, 0};
+      for (int n = 0; n < NT; ++n) x.v[n] = *(const v4i*)(vp + 16 * n * kv.page);
+    };
+    auto attend = [&](Tile& x, int kb) {
+      auto& kx = x.k;
+      auto& vx = x.v;
+      const int kb8 = x.ke, vb = x.ve;
+      const int keyv = kb + 16 * lg;
+      v4f sc[4];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const v4i kf = widen8<DT>(kc[2 * ks], kc[2 * ks + 1], 1.0f);
+      for (int t = 0; t < 4; ++t) {
+        sc[t] = v4f{0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < RT; ++t) sc[t][t8] = mma16<DT>(kf, qf[t][ks], sc[t][t8]);
+        for (int i = 0; i < KL; ++i) {
+          sc[t] = mma16<DT>(widen8<DT>(kx[t][i][0], kx[t][i][1], 1.0f), qf[2 * i], sc[t]);
+          sc[t] = mma16<DT>(widen8<DT>(kx[t][i][2], kx[t][i][3], 1.0f), qf[2 * i + 1], sc[t]);
         }
       }
-      // the values' reference exponent
+      // the scores; register 4 t + i is key keyv + 4 t + i
+      const float kscale = exp_byte(kb8) * a.scale_log2;
+      const bool edge = kb < klo || kb + kTile > khi, all = kb >= low && kb + kTile <= high;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = keyv + 4 * t + i;
+          const float x = all || (key >= low && key < high) ? sc[t][i] * kscale : -INFINITY;
+          sc[t][i] = x;
+          mx = fmaxf(mx, x);
+        }
+      // over the row's four lanes: the maximum, and the values' largest exponent
+      const bool seen = keyv < khi && keyv + 16 > klo;
       int bt = seen ? vb : 0;
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
       bt = max(bt, __shfl_xor(bt, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
       bt = max(bt, __shfl_xor(bt, 32));
       const int bnew = bt > bmax ? bt : bmax;
-      const float vfix = __builtin_ldexpf(1.0f, bmax - bnew < -126 ? -126 : bmax - bnew);
+      const int drop = bmax - bnew;
+      const float vfix = __builtin_ldexpf(1.0f, drop < -126 ? -126 : drop);
       bmax = bnew;
       int down = seen ? vb - bmax : 0;
       down = down < -126 ? -126 : down;
       const float vscale = __builtin_ldexpf(1.0f, down);
 
-      v4i pf[RT][4];
+      const float mn = fmaxf(m, mx);
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      const float alpha = __builtin_amdgcn_exp2f(m - ref);
+      m = mn;
+      float sum = 0.0f;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int t8 = 0; t8 < 8; ++t8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = keyv + 4 * t8 + i;
-            const float x = (key >= low[t] && key < high[t]) ? sc[t][t8][i] * kscale : -INFINITY;
-            sc[t][t8][i] = x;
-            mx = fmaxf(mx, x);
-          }
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m[t], mx);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float alpha = __builtin_amdgcn_exp2f(m[t] - ref);
-        m[t] = mn;
-        float sum = 0.0f;
-#pragma unroll
-        for (int t8 = 0; t8 < 8; ++t8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = __builtin_amdgcn_exp2f(sc[t][t8][i] - ref);
-            sc[t][t8][i] = p;
-            sum += p;
-          }
-        l[t] = l[t] * alpha + sum;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          pf[t][j] = v4i{(int)pack2_out<DT_F16>(sc[t][2 * j][0], sc[t][2 * j][1]),
-                         (int)pack2_out<DT_F16>(sc[t][2 * j][2], sc[t][2 * j][3]),
-                         (int)pack2_out<DT_F16>(sc[t][2 * j + 1][0], sc[t][2 * j + 1][1]),
-                         (int)pack2_out<DT_F16>(sc[t][2 * j + 1][2], sc[t][2 * j + 1][3])};
-        const float fix = alpha * vfix;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[t][n] *= fix;
-      }
-      // bytes of keys that no row sees are cleared: they may be anything, NaN codes included
-      const bool edge = kb < klo || kb + kTile > khi;
-      uint32_t keep[8];
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        uint32_t k = 0;
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = keyv + 4 * w + i;
-          k |= (key >= klo && key < khi) ? 0xffu << (8 * i) : 0u;
+          sc[t][i] = __builtin_amdgcn_exp2f(sc[t][i] - ref);
+          sum += sc[t][i];
         }
-        keep[w] = edge ? k : 0xffffffffu;
+      l = l * alpha + sum;
+      v4i pf[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        pf[j] = v4i{(int)pack2_out<DT_F16>(sc[2 * j][0], sc[2 * j][1]), (int)pack2_out<DT_F16>(sc[2 * j][2], sc[2 * j][3]),
+                    (int)pack2_out<DT_F16>(sc[2 * j + 1][0], sc[2 * j + 1][1]),
+                    (int)pack2_out<DT_F16>(sc[2 * j + 1][2], sc[2 * j + 1][3])};
+      const float fix = alpha * vfix;
+      if (__any(fix != 1.0f)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] *= fix;
+      }
+      if (edge) {
+        // codes of keys that no row sees may be anything, NaN included: the values' are cleared
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = keyv + 4 * w + i;
+            keep |= key >= klo && key < khi ? 0xffu << (8 * i) : 0u;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) vx[n][w] &= (int)keep;
+        }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const v4i x = *(const v4i*)(vp + (int64_t)(16 * n) * kv.page);
-        const v4i y = *(const v4i*)(vp + (int64_t)(16 * n) * kv.page + 16);
-        const int vc[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const v4i vf = widen8<DT_F16>(vc[2 * j] & (int)keep[2 * j], vc[2 * j + 1] & (int)keep[2 * j + 1], vscale);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[t][n] = mma16<DT_F16>(vf, pf[t][j], acc[t][n]);
-        }
+        acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][0], vx[n][1], vscale), pf[0], acc[n]);
+        acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][2], vx[n][3], vscale), pf[1], acc[n]);
       }
+    };
+    Tile one, two;
+    int kb = kb0 + wave * kTile;
+    pages(kb);
+    request(one, kb);
+    for (; kb < kb1; kb += 2 * kStride) {
+      request(two, kb + kStride);
+      __builtin_amdgcn_sched_barrier(0);
+      attend(one, kb);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kb + kStride >= kb1) break;
+      request(one, kb + 2 * kStride);
+      __builtin_amdgcn_sched_barrier(0);
+      attend(two, kb + kStride);
+      __builtin_amdgcn_sched_barrier(0);
     }
 
-    // join the four waves, one row tile at a time
+    // join the waves
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    const float vtrue = exp_byte(bmax);
+    __syncthreads();                 // the row tile before is read
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float lsum = l[t] + __shfl_xor(l[t], 16);
-      lsum += __shfl_xor(lsum, 32);
-      const float vtrue = exp_byte(bmax);
-      __syncthreads();
+    for (int n = 0; n < NT; ++n) *(v4f*)&s_acc[wave][lr][16 * n + 4 * lg] = acc[n] * vtrue;
+    if (lg == 0) {
+      s_ml[wave][lr][0] = m;
+      s_ml[wave][lr][1] = l;
+    }
+    __syncthreads();
+    // 16 threads per row, each D / 16 features
+    const int row16 = tid >> 4, part = tid & 15;
+    const int orw = r0 + row16;
+    if (tid < 256 && orw < rows) {
+      float mm = s_ml[0][row16][0];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) *(v4f*)&s_acc[wave][lr][16 * n + 4 * lg] = acc[t][n] * vtrue;
-      if (lg == 0) {
-        s_ml[wave][lr][0] = m[t];
-        s_ml[wave][lr][1] = lsum;
+      for (int w = 1; w < NW; ++w) mm = fmaxf(mm, s_ml[w][row16][0]);
+      const float ref = mm == -INFINITY ? 0.0f : mm;
+      float f[NW], ll = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(s_ml[w][row16][0] - ref);
+        ll += f[w] * s_ml[w][row16][1];
       }
-      __syncthreads();
-      // 16 threads per row, each D / 16 consecutive features
-      const int row16 = tid >> 4, part = tid & 15;
-      const int row = r0 + 16 * t + row16;
-      if (row < rows) {
-        float mm = s_ml[0][row16][0];
+      const int otok = orw / group, oh = orw - otok * group;
+      const int64_t orow = (int64_t)(sp.first + otok) * a.heads + head * group + oh;
+      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, s_ml[w][row16][0]);
-        const float ref = mm == -INFINITY ? 0.0f : mm;
-        float f[kWaves], ll = 0.0f;
+      for (int e = 0; e < D / 64; ++e) {
+        const int d = part * 4 + e * 64;
+        v4f o = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          f[w] = __builtin_amdgcn_exp2f(s_ml[w][row16][0] - ref);
-          ll += f[w] * s_ml[w][row16][1];
+        for (int w = 0; w < NW; ++w) o += *(const v4f*)&s_acc[w][row16][d] * f[w];
+        if (split_out) {
+          *(v4f*)(a.part + ((int64_t)split * kv.tokens * a.heads + orow) * D + d) = o;
+        } else {
+          o *= inv;
+          *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
         }
-        const int tok = row / group, hq = row - tok * group;
-        const int64_t orow = (int64_t)(sp.first + tok) * a.heads + head * group + hq;
-        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-#pragma unroll
-        for (int e = 0; e < D / 16; e += 4) {
-          const int d = part * 4 + (e / 4) * 64;
-          v4f o = {0, 0, 0, 0};
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) o += *(const v4f*)&s_acc[w][row16][d] * f[w];
-          if (split_out) {
-            *(v4f*)(a.part + ((int64_t)split * kv.tokens * a.heads + orow) * D + d) = o;
-          } else {
-            o *= inv;
-            *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
-          }
-        }
-        if (part == 0) {
-          if (split_out) {
-            float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
-            ml[0] = mm;
-            ml[1] = ll;
-          } else if (a.lse) {
-            a.lse[orow] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -INFINITY;
-          }
+      }
+      if (part == 0) {
+        if (split_out) {
+          float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
+          ml[0] = mm;
+          ml[1] = ll;
+        } else if (a.lse) {
+          a.lse[orow] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -INFINITY;
         }
       }
     }
@@ -314,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_rows(const AttnArgs a, int ro
 // once, two steps ahead, widened by the thread that read them and put into
 // LDS (two buffers), from where every wave reads MFMA operands; widened by each
 // wave for itself the conversions are a third of all vector instructions
-// (675 against 4xx us for a prompt of 8192 tokens, 32 heads over 8).
+// (675 against 657 us for a prompt of 8192 tokens, 32 heads over 8).
 //
 // v_mfma_f32_32x32x16: S^T = K Q^T in two 32-key tiles, lane (q, h) (q = lane %
 // 32, h = lane / 32) holding row q; tile T's row 8 a + 4 h + b is key 32 h +
@@ -696,34 +716,55 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
   }
 }
 
-// Joins the splits of a row, in their order: one wave per row of a sequence.
+// Joins the splits of a row: one workgroup per row of a sequence.  Its threads
+// take 4 features each of every G-th split (G = 1024 / D groups), then join the
+// groups through LDS; always in the same order.
+constexpr int kMaxSplits = 256;
 template <int D, int DT>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks, int splits) {
+  constexpr int G = 1024 / D;
+  __shared__ float s_f[kMaxSplits], s_top[4], s_sum[4];
+  __shared__ __attribute__((aligned(16))) float s_o[G][D];
   const Span sp = span_of(a, blockIdx.x / blocks);
-  const int lane = threadIdx.x & 63;
+  const int tid = threadIdx.x, wave = tid >> 6;
   const int64_t rows = (int64_t)a.kv.tokens * a.heads, mine = (int64_t)sp.n * a.heads;
-  for (int64_t r = (int64_t)(blockIdx.x % blocks) * 4 + (threadIdx.x >> 6); r < mine; r += (int64_t)blocks * 4) {
+  for (int64_t r = blockIdx.x % blocks; r < mine; r += blocks) {
     const int64_t row = (int64_t)sp.first * a.heads + r;
-    float mm = -INFINITY;
-    for (int i = lane; i < splits; i += 64) mm = fmaxf(mm, a.part_ml[(i * rows + row) * 2]);
-    mm = wave_max(mm);
-    const float ref = mm == -INFINITY ? 0.0f : mm;
-    constexpr int E = D / 64;
-    float o[E] = {};
-    float ll = 0.0f;
-    for (int i = 0; i < splits; ++i) {
-      const float* ml = a.part_ml + (i * rows + row) * 2;
-      const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
-      ll += f * ml[1];
-      const float* p = a.part + (i * rows + row) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * p[e];
+    // thread i: split i's maximum and sum
+    float mi = -INFINITY, li = 0.0f;
+    if (tid < splits) {
+      const float* ml = a.part_ml + (tid * rows + row) * 2;
+      mi = ml[0];
+      li = ml[1];
     }
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const int g = tid / (D / 4), d = tid % (D / 4) * 4;
+    const float top = wave_max(mi);
+    __syncthreads();                       // the row before is read
+    if ((tid & 63) == 0) s_top[wave] = top;
+    __syncthreads();
+    const float mm = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    const float f = __builtin_amdgcn_exp2f(mi - ref);
+    s_f[tid] = f;
+    float ls = f * li;
 #pragma unroll
-    for (int e = 0; e < E; ++e) store_out<DT>(a.out, row * D + lane * E + e, o[e] * inv);
-    if (a.lse && lane == 0)
-      a.lse[row] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -INFINITY;
+    for (int o = 1; o < 64; o <<= 1) ls += __shfl_xor(ls, o);
+    if ((tid & 63) == 0) s_sum[wave] = ls;
+    __syncthreads();
+    const float ll = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+    v4f o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = g; i < splits; i += G) o += *(const v4f*)(a.part + (i * rows + row) * D + d) * s_f[i];
+    *(v4f*)&s_o[g][d] = o;
+    __syncthreads();
+    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    if (tid < D) {
+      float v = s_o[0][tid];
+#pragma unroll
+      for (int i = 1; i < G; ++i) v += s_o[i][tid];
+      store_out<DT>(a.out, row * D + tid, v * inv);
+    }
+    if (a.lse && tid == 0) a.lse[row] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -745,12 +786,17 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
           : dim == 256 || (dim == 64 && pairs * ((rows + 255) / 256) < 256) ? 128 : 256;
   p.blocks = (rows + p.per - 1) / p.per;
   int64_t keys = max_kv;
-  if (window > 0 && window + max_q + kTile < keys) keys = window + max_q + kTile;
+  if (window > 0 && window + max_q + 2 * kTile < keys) keys = window + max_q + 2 * kTile;
   const int64_t groups = pairs * p.blocks;
-  const int64_t step = kWaves * kTile;
-  int64_t want = p.per == kSmallRows ? (1024 + groups - 1) / groups : groups >= 192 ? 1 : 512 / groups;
+  const int64_t step = 512;
+  // Splits to fill the chip, none where the sequences and heads do it alone (64 sequences, 8 kv heads,
+  // up to 4099 keys: 74 us whole, 77 + 5 in 1024-key shares), but none longer than 8192 keys either,
+  // so that one long sequence among many does not hold up the rest.
+  int64_t want = p.per == kSmallRows ? (groups >= 512 ? 1 : 1024 / groups) : groups >= 192 ? 1 : 512 / groups;
+  want = want < keys / 8192 ? keys / 8192 : want;
   const int64_t most = (keys + step - 1) / step;
   want = want > most ? most : want;
+  want = want > kMaxSplits ? kMaxSplits : want;
   want = want < 1 ? 1 : want;
   int64_t c = ((keys + want - 1) / want + step - 1) / step * step;
   c = c < 2 * step ? 2 * step : c;     // a shorter share costs the join more than it saves
@@ -771,7 +817,13 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   const int blocks = (int)p.blocks;
   if (p.per == kSmallRows) {
     const dim3 grid((unsigned)p.splits, (unsigned)a.kv.kv_heads, (unsigned)(p.blocks * a.kv.seqs));
-    k_attn_rows<D, 1, DT><<<grid, kThreads, 0, st>>>(a, blocks, p.chunk);
+    // 8 waves (half as many tiles one after the other: 513 keys, 8 kv heads, 11.0 against 9.2 us) where
+    // every workgroup has a CU to itself
+    if (D < 256 && (int64_t)grid.x * grid.y * grid.z <= 256) {
+      if constexpr (D < 256) k_attn_rows<D, DT, 8><<<grid, 512, 0, st>>>(a, blocks, p.chunk);
+    } else {
+      k_attn_rows<D, DT, 4><<<grid, 256, 0, st>>>(a, blocks, p.chunk);
+    }
   } else {
     const unsigned grid = (unsigned)(p.blocks * a.kv.seqs * a.kv.kv_heads * p.splits);
     if constexpr (D != 128)
@@ -781,7 +833,7 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  int64_t jb = ((int64_t)a.max_q * a.heads + 3) / 4;
+  int64_t jb = (int64_t)a.max_q * a.heads;
   const int64_t limit = ((int64_t)1 << 30) / a.kv.seqs;
   jb = jb > limit ? limit : jb;
   k_attn_join<D, DT><<<(unsigned)(jb * a.kv.seqs), 256, 0, st>>>(a, (int)jb, p.splits);
