@@ -364,7 +364,46 @@ def test_other_stream_and_graph():
         (torch.randn(256, 256, device=DEV) @ torch.randn(256, 256, device=DEV)).sum().item()
 
 
-# ---------------------------------------------------------------- refusals of the binding
+# ---------------------------------------------------------------- the binding
+def test_compiled_and_interpreted_calls_agree():
+    """The compiled half of the binding takes ordinary arguments and gives what the checked path gives."""
+    fast = q8._fast()
+    rng = np.random.default_rng(4)
+    table, pages = table_of(rng, [300, 90], 64)
+    base = random_cache(rng, pages, 2, 64, 128)
+    _, batch = batch_of([2, 1], [300, 90], table)
+    qkv = torch.from_numpy(rng.standard_normal((3, 12, 128)).astype(np.float32)).to(BF).to(DEV)
+    cos, sin = (torch.from_numpy(a).to(DEV) for a in tables_of_angles(300, 128))
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    got = []
+    for compiled in (True, False):
+        cache = device(base)
+        if compiled:
+            r = fast.kv_append(k, v, cache, batch, q, cos, sin, False, None)
+            assert isinstance(r, torch.Tensor)
+            o = fast.attention_kv8(r, cache, batch, None, True, 0, None)
+            assert isinstance(o, torch.Tensor)
+        else:
+            hold = q8._FAST
+            q8._FAST = type("none", (), {n: staticmethod(lambda *a: NotImplemented)
+                                         for n in ("kv_append", "attention_kv8", "linear_fp8_block")})
+            try:
+                r = q8.q8_kv_append(k, v, cache, batch, q=q, cos=cos, sin=sin)
+                o = q8.q8_attention_kv8(r, cache, batch)
+            finally:
+                q8._FAST = hold
+        got.append([r, o, *cache])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    # what the call refuses comes back as its status, what is not its kind of argument as NotImplemented
+    assert fast.attention_kv8(q, device(base), batch, None, True, -1, None) == _lib.Q8_ERR_BAD_ARG
+    assert fast.attention_kv8(q.cpu(), device(base), batch, None, True, 0, None) is NotImplemented
+    assert fast.attention_kv8(q, device(base), batch, "x", True, 0, None) is NotImplemented
+    assert fast.kv_append(k, v, device(base), batch, None, None, sin, False, None) is NotImplemented
+    with pytest.raises(TypeError):
+        fast.kv_append(k, v)
+
+
 def test_binding_refusals():
     cache = q8.q8_kv_cache(4, 2, 64, page=32, device=DEV)
     _, batch = batch_of([2], [2], [[0, 1]])

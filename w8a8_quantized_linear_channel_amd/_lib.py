@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq8.so")
 
 # enum values, as in include/q8.h
 Q8_OK = 0
+Q8_ERR_BAD_ARG = 5
 STATUS_NAMES = {
     0: "Q8_OK", 1: "Q8_ERR_NULL_PTR", 2: "Q8_ERR_BAD_SHAPE", 3: "Q8_ERR_BAD_DTYPE",
     4: "Q8_ERR_BAD_FORMAT", 5: "Q8_ERR_BAD_ARG", 6: "Q8_ERR_ALIGN", 7: "Q8_ERR_WORKSPACE",

@@ -1,4 +1,5 @@
-"""Build libq8.so in-tree with hipcc for gfx950.
+"""Build libq8.so in-tree with hipcc for gfx950, and _binding.so, the
+compiled half of the torch binding.
 
 Every source under csrc/ is compiled to an object under _build/ (in
 parallel), then linked into w8a8_quantized_linear_channel_amd/libq8.so.
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libq8.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = "gfx950"
 COMMON = [
@@ -53,6 +55,18 @@ def _run(cmd, verbose):
         print(err, file=sys.stderr)
 
 
+def _binding_object_cmd(obj: str):
+    """Host C++ against the interpreter's and torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(), INCLUDE]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return ["g++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-Wno-unknown-pragmas", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+            *[f for d in inc for f in ("-isystem", d)], "-c", os.path.join(PKG, "binding.cpp"), "-o", obj]
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     cc = hipcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -65,11 +79,19 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
         flags = COMMON + HIP_ONLY if f.endswith(".hip") else COMMON + ["-D__HIP_PLATFORM_AMD__"]
         lang = ["-x", "hip"] if f.endswith(".hip") else []
         cmds.append([cc] + lang + flags + ["-c", os.path.join(CSRC, f), "-o", obj])
+    binding_obj = os.path.join(BUILD, "binding.cpp.o")
+    cmds.insert(0, _binding_object_cmd(binding_obj))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         list(ex.map(lambda c: _run(c, verbose), cmds))
     tmp = LIB + ".tmp"
     _run([cc, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp], verbose)
     os.replace(tmp, LIB)
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-fPIC", binding_obj, f"-L{PKG}", "-l:libq8.so", f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+          "-Wl,-rpath,$ORIGIN", "-o", tmp], verbose)
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -431,6 +431,28 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+_FAST = None
+
+
+def _fast():
+    """The compiled half of this binding (binding.cpp), which does the checks and the call of the
+    latency-bound functions; a result of NotImplemented means an argument it does not take, and the
+    checks below say what is wrong with it."""
+    global _FAST
+    if _FAST is None:
+        _lib.lib()                      # says how to build what is missing
+        from . import _binding
+        _FAST = _binding
+    return _FAST
+
+
+def _result(func: str, r):
+    """A compiled call's result, or its C status as an exception."""
+    if type(r) is int:
+        _lib.check(func, r)
+    return r
+
+
 def _is(t, dtype, shape, index: int) -> bool:
     """A dense tensor of this dtype and shape on device `index` (the check of the calls whose
     latency counts; _need says what is wrong where this is False)."""
@@ -498,6 +520,9 @@ def q8_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatc
     keys rotated by cos, sin [positions, rot_dim / 2] if given; returns the
     rotated queries of q [T, heads, dim], or None without q.  k, v and q may be
     slices of one projection's output (any token stride)."""
+    r = _fast().kv_append(k, v, cache, batch, q, cos, sin, interleaved, out)
+    if r is not NotImplemented:
+        return _result("q8_kv_append", r)
     index, dev = _cuda_index(k, "k"), k.device
     P, Hkv, page, D, S, max_pages = _check_kv(cache, batch, dev, index)
     dt = k.dtype
@@ -550,6 +575,10 @@ def q8_attention_kv8(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Opt
     """Attention of the new queries q [T, heads, dim] (bf16 or fp16, any token
     stride) over the cache; scale defaults to 1/sqrt(dim).  Returns out
     [T, heads, dim] (and the log-sum-exp float32 [T, heads] if lse)."""
+    if not lse and workspace is None:
+        r = _fast().attention_kv8(q, cache, batch, scale, causal, window, out)
+        if r is not NotImplemented:
+            return _result("q8_attention_kv8", r)
     index, dev = _cuda_index(q, "q"), q.device
     P, Hkv, page, D, S, max_pages = _check_kv(cache, batch, dev, index)
     dt = q.dtype
@@ -645,6 +674,10 @@ def q8_linear_fp8_block(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor
     """Linear layer with block-scaled FP8 weights (from q8_quantize_weight_block)
     and activations quantized per token and 128 features; bf16 or fp16 out
     (default: x's dtype, bf16 for a float32 x)."""
+    if workspace is None:
+        r = _fast().linear_fp8_block(x, wq, w_scale, bias, out_dtype, out)
+        if r is not NotImplemented:
+            return _result("q8_linear_fp8_block", r)
     index, dev = _cuda_index(x, "x"), x.device
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
