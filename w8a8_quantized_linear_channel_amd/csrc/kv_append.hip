@@ -42,34 +42,62 @@ __device__ __forceinline__ void store8(void* base, int64_t off, const float* v) 
   }
 }
 
-// The 8 rotated features 8c .. 8c+7 of the head at element offset `off`.  Every
-// product and the sum are rounded on their own (no contraction), so the codes
-// do not depend on how the compiler pairs them.
-template <int DT>
-__device__ __forceinline__ void load_rotated(const AppendArgs& a, const void* x, int64_t off, int c, int pos, float* v) {
-#pragma clang fp contract(off)
-  load8<DT>(x, off + 8 * c, v);
-  if (8 * c >= a.rot) return;
+// cos and sin of the 8 features 8c .. 8c+7 of a head at a position, as their rotation uses them:
+// 8 of each for pairs (i, i + r), 4 of each for pairs (2 i, 2 i + 1).
+struct Turn {
+  float co[8], si[8];
+};
+__device__ __forceinline__ void load_turn(const AppendArgs& a, int c, int pos, Turn& t) {
   const int half = a.rot >> 1;
   const int64_t row = (int64_t)(pos < a.positions ? pos : a.positions - 1) * half;
   if (a.interleaved) {
-    const v4f co = *(const v4f*)(a.cos + row + 4 * c), si = *(const v4f*)(a.sin + row + 4 * c);
+    Chunk<DT_F32>::decode(*(const v4i*)(a.cos + row + 4 * c), t.co);
+    Chunk<DT_F32>::decode(*(const v4i*)(a.sin + row + 4 * c), t.si);
+  } else {
+    const int j = 8 * c < half ? 8 * c : 8 * c - half;
+    load8<DT_F32>(a.cos, row + j, t.co);
+    load8<DT_F32>(a.sin, row + j, t.si);
+  }
+}
+// Every product and the sum are rounded on their own (no contraction), so the codes do not depend on
+// how the compiler pairs them.  w: the partner features (pairs (i, i + r) only), low: v is the first
+// of the two.
+__device__ __forceinline__ void turn8(const Turn& t, bool interleaved, bool low, float* v, const float* w) {
+#pragma clang fp contract(off)
+  if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float p = v[2 * i], r = v[2 * i + 1];
-      v[2 * i] = p * co[i] - r * si[i];
-      v[2 * i + 1] = r * co[i] + p * si[i];
+      v[2 * i] = p * t.co[i] - r * t.si[i];
+      v[2 * i + 1] = r * t.co[i] + p * t.si[i];
     }
   } else {
-    const bool low = 8 * c < half;
-    const int j = low ? 8 * c : 8 * c - half;
-    float w[8], co[8], si[8];
-    load8<DT>(x, off + (low ? 8 * c + half : 8 * c - half), w);
-    load8<DT_F32>(a.cos, row + j, co);
-    load8<DT_F32>(a.sin, row + j, si);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = low ? v[i] * co[i] - w[i] * si[i] : v[i] * co[i] + w[i] * si[i];
+    for (int i = 0; i < 8; ++i) {
+      const float side = low ? -w[i] : w[i];
+      v[i] = v[i] * t.co[i] + side * t.si[i];      // (a cos - b sin: the negated product rounds alike)
+    }
   }
+}
+// The features 8c .. 8c+7 of the head at element offset `off`, rotated.  Lanes whose features are not
+// rotated load the angles of others and leave them unused: a branch here makes the loads of several
+// tokens wait for one another.
+template <int DT>
+__device__ __forceinline__ void load_rotated(const AppendArgs& a, const void* x, int64_t off, int c, int pos, float* v) {
+  load8<DT>(x, off + 8 * c, v);
+  if (a.rot == 0) return;                                    // uniform
+  const int half = a.rot >> 1;
+  const bool turned = 8 * c < a.rot, low = 8 * c < half;
+  const int ct = turned ? c : 0;
+  Turn t;
+  float w[8] = {}, u[8];
+  if (!a.interleaved) load8<DT>(x, off + (turned ? (low ? 8 * c + half : 8 * c - half) : 0), w);
+  load_turn(a, ct, pos, t);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = v[e];
+  turn8(t, a.interleaved, low, u, w);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = turned ? u[e] : v[e];
 }
 
 // The exponent byte of a page and head: the least b with amax <= 448 2^(b - 127).
@@ -116,8 +144,12 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const int last = (hi - 1) / B;
   for (int lp = lo / B + j0; lp <= last; lp += a.reach) {
+    // the page and the scale that it has are on their way while the new values are read
     const int page = kv.table[(int64_t)s * kv.max_pages + lp];
-    if (page < 0 || page >= kv.num_pages) continue;
+    const bool here = page >= 0 && page < kv.num_pages;
+    const int64_t ph = (int64_t)(here ? page : 0) * kv.kv_heads + (have ? head : 0);
+    uint8_t* const exps = (is_v ? kv.ve : kv.ke) + ph;
+    const int had = *exps;
     const int base = lp * B + 16 * tg;
     int i0 = lo - base, i1 = hi - base;
     i0 = i0 < 0 ? 0 : (i0 > 16 ? 16 : i0);
@@ -125,13 +157,38 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     const bool active = have && patch < SH::kPatches;
     if (!active) i0 = i1 = 0;
     auto row = [&](int i) { return (int64_t)(first + (base + i - past)) * stride + (int64_t)head * D; };
+    // more than two new tokens in the patch: all 16 places at once (those without a new token repeat
+    // one that is, and are not stored); one or two, as in decoding: one after the other
+    const bool many = i1 - i0 > 2;
     float amax = 0.0f;
-    for (int i = i0; i < i1; ++i) {
-      float v[8];
-      if (is_v) load8<DT>(x, row(i) + 8 * c, v);
-      else load_rotated<DT>(a, x, row(i), c, base + i, v);
+    // Read once for the maximum and once more (from the caches) for the codes: kept in registers instead,
+    // 16 x 8 floats leave too few waves for the queries' copy in the same launch.
+    auto four = [&](int i, float (*v)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+      for (int j = 0; j < 4; ++j) {
+        const int k = i + j < i0 ? i0 : (i + j < i1 ? i + j : i1 - 1);
+        if (is_v) load8<DT>(x, row(k) + 8 * c, v[j]);
+        else load_rotated<DT>(a, x, row(k), c, base + k, v[j]);
+      }
+    };
+    if (many) {
+#pragma unroll 1
+      for (int i = 0; i < 16; i += 4) {
+        float v[4][8];
+        four(i, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[j][e]));
+      }
+    } else {
+      for (int i = i0; i < i1; ++i) {
+        float v[8];
+        if (is_v) load8<DT>(x, row(i) + 8 * c, v);
+        else load_rotated<DT>(a, x, row(i), c, base + i, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+      }
     }
     amax = wave_max(amax);
     if constexpr (SH::kItemWaves > 1) {
@@ -141,112 +198,167 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
 #pragma unroll
       for (int w = 0; w < SH::kItemWaves; ++w) amax = fmaxf(amax, red[wave / SH::kItemWaves * SH::kItemWaves + w]);
     }
-    if (!active) continue;
-    uint8_t* const exps = (is_v ? kv.ve : kv.ke) + (int64_t)page * kv.kv_heads + head;
+    if (!active || !here) continue;
     const bool fresh = lo <= lp * B;               // no token of the page is older than this call's
-    const int want = exponent_byte(amax), had = *exps;
+    const int want = exponent_byte(amax);
     const int b = fresh ? want : (had > want ? had : want);
     const int shift = fresh ? 0 : had - b;
     if (patch == 0 && b != had) *exps = (uint8_t)b;
-    const int64_t at = ((int64_t)page * kv.kv_heads + head) * (D * B);
-    if (!is_v) {
-      uint8_t* const codes = kv.k + at + (int64_t)(16 * tg) * D + 8 * c;
-      if (shift < 0)
+    const int64_t at = ph * (D * B);
+    uint8_t* const kc = kv.k + at + (int64_t)(16 * tg) * D + 8 * c;
+    uint8_t* const vc = kv.v + at + (int64_t)(8 * c) * B + 16 * tg;
+    // old tokens of the patch at the new scale
+    if (shift < 0 && i0 > 0) {
+      if (!is_v) {
         for (int i = 0; i < i0; ++i) {
-          v2i* p = (v2i*)(codes + i * D);
+          v2i* p = (v2i*)(kc + i * D);
           const v2i o = *p;
           *p = v2i{(int)rescale4((uint32_t)o[0], shift), (int)rescale4((uint32_t)o[1], shift)};
         }
-      for (int i = i0; i < i1; ++i) {
-        float v[8];
-        load_rotated<DT>(a, x, row(i), c, base + i, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], 127 - b);
-        *(v2i*)(codes + i * D) = v2i{(int)pack4_e4m3(v[0], v[1], v[2], v[3]), (int)pack4_e4m3(v[4], v[5], v[6], v[7])};
-      }
-    } else {
-      uint8_t* const codes = kv.v + at + (int64_t)(8 * c) * B + 16 * tg;
-      if (shift < 0 && i0 > 0) {
-        // old tokens of the patch: 16 bytes of each feature, those past i0 kept
+      } else {
+        // 16 bytes of each feature, those past i0 kept
         for (int e = 0; e < 8; ++e) {
-          v4i o = *(const v4i*)(codes + e * B);
+          v4i o = *(const v4i*)(vc + e * B);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const int n = i0 - 4 * w;                             // old tokens in this word
             const uint32_t mask = n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
             o[w] = (int)((rescale4((uint32_t)o[w], shift) & mask) | ((uint32_t)o[w] & ~mask));
           }
-          *(v4i*)(codes + e * B) = o;
+          *(v4i*)(vc + e * B) = o;
         }
       }
-      if (i0 == 0 && i1 == 16) {
+    }
+    auto codes = [&](const float* v, uint32_t& q0, uint32_t& q1) {
+      float u[8];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t q[4][2];
+      for (int e = 0; e < 8; ++e) u[e] = __builtin_ldexpf(v[e], 127 - b);
+      q0 = pack4_e4m3(u[0], u[1], u[2], u[3]);
+      q1 = pack4_e4m3(u[4], u[5], u[6], u[7]);
+    };
+    if (many) {
+      if (!is_v) {
+#pragma unroll 1
+        for (int i = 0; i < 16; i += 4) {
+          float v[4][8];
+          four(i, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v[8];
-            load8<DT>(x, row(4 * w + i) + 8 * c, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], 127 - b);
-            q[i][0] = pack4_e4m3(v[0], v[1], v[2], v[3]);
-            q[i][1] = pack4_e4m3(v[4], v[5], v[6], v[7]);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t sel = 8 * (e & 3);
-            uint32_t r = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r |= ((q[i][e >> 2] >> sel) & 0xffu) << (8 * i);
-            *(uint32_t*)(codes + e * B + 4 * w) = r;
+          for (int j = 0; j < 4; ++j) {
+            uint32_t q0, q1;
+            codes(v[j], q0, q1);
+            if (i + j >= i0 && i + j < i1) *(v2i*)(kc + (i + j) * D) = v2i{(int)q0, (int)q1};
           }
         }
       } else {
-        for (int i = i0; i < i1; ++i) {
-          float v[8];
-          load8<DT>(x, row(i) + 8 * c, v);
+        // 16 tokens of a feature together: 4 x 4 byte transpositions
+        uint32_t o[8][4];                          // [feature][four tokens]
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], 127 - b);
-          const uint32_t q0 = pack4_e4m3(v[0], v[1], v[2], v[3]), q1 = pack4_e4m3(v[4], v[5], v[6], v[7]);
+        for (int w = 0; w < 4; ++w) {
+          float v[4][8];
+          uint32_t q[4][2];
+          four(4 * w, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) codes[e * B + i] = (uint8_t)((e < 4 ? q0 : q1) >> (8 * (e & 3)));
+          for (int j = 0; j < 4; ++j) codes(v[j], q[j][0], q[j][1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t l01 = __builtin_amdgcn_perm(q[1][h], q[0][h], 0x05010400u), h01 = __builtin_amdgcn_perm(q[1][h], q[0][h], 0x07030602u);
+            const uint32_t l23 = __builtin_amdgcn_perm(q[3][h], q[2][h], 0x05010400u), h23 = __builtin_amdgcn_perm(q[3][h], q[2][h], 0x07030602u);
+            o[4 * h][w] = __builtin_amdgcn_perm(l23, l01, 0x05040100u);
+            o[4 * h + 1][w] = __builtin_amdgcn_perm(l23, l01, 0x07060302u);
+            o[4 * h + 2][w] = __builtin_amdgcn_perm(h23, h01, 0x05040100u);
+            o[4 * h + 3][w] = __builtin_amdgcn_perm(h23, h01, 0x07060302u);
+          }
+        }
+        if (i1 - i0 < 16) {
+          // bytes of places without a new token stay (the patch is this thread's alone)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t put = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) put |= 4 * w + j >= i0 && 4 * w + j < i1 ? 0xffu << (8 * j) : 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e][w] = (o[e][w] & put) | (*(const uint32_t*)(vc + e * B + 4 * w) & ~put);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) *(v4i*)(vc + e * B) = v4i{(int)o[e][0], (int)o[e][1], (int)o[e][2], (int)o[e][3]};
+      }
+    } else {
+      for (int i = i0; i < i1; ++i) {
+        float v[8];
+        uint32_t q0, q1;
+        if (is_v) load8<DT>(x, row(i) + 8 * c, v);
+        else load_rotated<DT>(a, x, row(i), c, base + i, v);
+        codes(v, q0, q1);
+        if (!is_v) {
+          *(v2i*)(kc + i * D) = v2i{(int)q0, (int)q1};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) vc[e * B + i] = (uint8_t)((e < 4 ? q0 : q1) >> (8 * (e & 3)));
         }
       }
     }
   }
 }
 
-// The queries of one sequence: one (token, head, 8 features) per thread.
+// The queries of one sequence: one token, 8 features (with pairs (i, i + r): both groups of 8 of a
+// pair) and `span` heads per thread, which share their cosines and sines.
 template <int DT, int D>
-__device__ void rotate_queries(const AppendArgs& a, int s, int block, int blocks) {
+__device__ void rotate_queries(const AppendArgs& a, int s, int block, int blocks, int span) {
   const KvView& kv = a.kv;
   int end = kv.q_start[s + 1], first = kv.q_start[s];
   end = end < 0 ? 0 : (end > kv.tokens ? kv.tokens : end);
   first = first < 0 ? 0 : (first > end ? end : first);
   const int len = kv.kv_len[s], past = (len < 0 ? 0 : len) - (end - first);
-  const int per = a.heads * (D / 8);
+  const int pairs = a.interleaved ? 0 : a.rot >> 4;          // units that are pairs of groups
+  const int units = D / 8 - pairs, spans = (a.heads + span - 1) / span;
+  const int per = units * spans;
   const int64_t all = (int64_t)(end - first) * per;
   for (int64_t i = (int64_t)block * kThreads + threadIdx.x; i < all; i += (int64_t)blocks * kThreads) {
     const int t = (int)(i / per), r = (int)(i - (int64_t)t * per);
-    const int h = r / (D / 8), c = r % (D / 8);
+    const int h0 = r / units * span, u = r % units;
+    const bool pair = u < pairs;
+    const int c = pair ? u : u + pairs;                      // (first) group of 8 features
+    const bool turned = 8 * c < a.rot;
     const int pos = past + t < 0 ? 0 : past + t;
-    float v[8];
-    load_rotated<DT>(a, a.q, (int64_t)(first + t) * a.q_stride + (int64_t)h * D, c, pos, v);
-    store8<DT>(a.q_out, ((int64_t)(first + t) * a.heads + h) * D + 8 * c, v);
+    Turn tu;
+    if (turned) load_turn(a, c, pos, tu);
+    const int64_t from = (int64_t)(first + t) * a.q_stride + 8 * c, to = (int64_t)(first + t) * a.heads * D + 8 * c;
+    const int h1 = h0 + span < a.heads ? h0 + span : a.heads;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h) {
+      float v[8], w[8];
+      load8<DT>(a.q, from + (int64_t)h * D, v);
+      if (pair) {
+        load8<DT>(a.q, from + (int64_t)h * D + 8 * pairs, w);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = v[e];
+        turn8(tu, false, true, v, w);
+        turn8(tu, false, false, w, x);
+        store8<DT>(a.q_out, to + (int64_t)h * D + 8 * pairs, w);
+      } else if (turned) {
+        turn8(tu, true, true, v, w);
+      }
+      store8<DT>(a.q_out, to + (int64_t)h * D, v);
+    }
   }
 }
 
 template <int DT, int D, int B>
-__global__ __launch_bounds__(kThreads) void k_kv_append(const AppendArgs a, int kv_blocks, int groups, int q_blocks) {
+__global__ __launch_bounds__(kThreads, 4) void k_kv_append(const AppendArgs a, int kv_blocks, int groups, int q_blocks,
+                                                            int span) {
   __shared__ float red[kThreads / 64];
-  int b = blockIdx.x;
-  if (b < kv_blocks) {
-    const int group = b % groups;
-    b /= groups;
-    append_pages<DT, D, B>(a, b / a.reach, b % a.reach, group, red);
+  // the pages' workgroups (few bytes, several round trips) spread evenly among the queries' (a stream):
+  // workgroup i is number floor(i kv / all) of the pages' where that number grows behind it
+  const int64_t all = gridDim.x, i = blockIdx.x;
+  const int before = (int)(i * kv_blocks / all), after = (int)((i + 1) * kv_blocks / all);
+  if (after > before) {
+    const int b = before / groups;
+    append_pages<DT, D, B>(a, b / a.reach, b % a.reach, before % groups, red);
   } else {
-    b -= kv_blocks;
-    rotate_queries<DT, D>(a, b / q_blocks, b % q_blocks, q_blocks);
+    const int b = (int)i - before;
+    rotate_queries<DT, D>(a, b / q_blocks, b % q_blocks, q_blocks, span);
   }
 }
 
@@ -256,14 +368,17 @@ hipError_t launch_shape(const AppendArgs& a, hipStream_t st) {
   const int64_t groups = (2 * a.kv.kv_heads + SH::kItems - 1) / SH::kItems;
   const int64_t kv_blocks = (int64_t)a.kv.seqs * a.reach * groups;
   int64_t q_blocks = 0;
+  // heads of a thread: one where there are few tokens (latency), eight that share their angles elsewhere
+  const int span = (int64_t)a.max_q * a.kv.seqs >= 1024 ? 8 : 1;
   if (a.q) {
-    q_blocks = ((int64_t)a.max_q * a.heads * (D / 8) + kThreads - 1) / kThreads;
+    const int64_t units = D / 8 - (a.interleaved ? 0 : a.rot >> 4), spans = (a.heads + span - 1) / span;
+    q_blocks = ((int64_t)a.max_q * units * spans + kThreads - 1) / kThreads;
     const int64_t most = ((int64_t)1 << 30) / a.kv.seqs;
     q_blocks = q_blocks > most ? most : q_blocks;
   }
   if (kv_blocks + q_blocks * a.kv.seqs > ((int64_t)1 << 31) - 1) return hipErrorInvalidValue;
-  k_kv_append<DT, D, B><<<(unsigned)(kv_blocks + q_blocks * a.kv.seqs), kThreads, 0, st>>>(a, (int)kv_blocks, (int)groups,
-                                                                                          q_blocks > 0 ? (int)q_blocks : 1);
+  k_kv_append<DT, D, B><<<(unsigned)(kv_blocks + q_blocks * a.kv.seqs), kThreads, 0, st>>>(
+      a, (int)kv_blocks, (int)groups, q_blocks > 0 ? (int)q_blocks : 1, span);
   return hipGetLastError();
 }
 
