@@ -5,17 +5,19 @@
 // Work is cut by page: one (sequence, touched page, kv head, K or V) is one
 // item, so the scale of a page and head is decided in one place, without
 // atomics, whatever the number of new tokens in it.  An item's tokens x
-// features are patches of 16 tokens x 8 features, one per thread: a token's
+// features are patches of 8 tokens x 8 features, one per thread: a token's
 // 8 features are one 16-byte load, K goes out as 8 bytes per token, and V,
-// stored with the tokens innermost, as 16 bytes per feature, with no
-// transposition through LDS.
+// stored with the tokens innermost, as 8 bytes per feature, with no
+// transposition through LDS.  (Patches of 16 tokens: half the waves, each
+// with twice the round trips, 110 against 105 us for the keys and values of
+// 15 thousand tokens beside their queries.)
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
 
 namespace q8 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kPatch = 8;         // tokens of a patch
 
 // 8 consecutive elements as floats
 template <int DT>
@@ -117,10 +119,10 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, int shift) {
 template <int DT, int D, int B>
 struct Shape {
   static constexpr int kCols = D / 8;                            // 8-feature chunks of a head
-  static constexpr int kPatches = (B / 16) * kCols;              // of one item
+  static constexpr int kPatches = (B / kPatch) * kCols;          // of one item
+  static constexpr int kThreads = kPatches > 256 ? kPatches : 256;
   static constexpr int kItemWaves = kPatches > 64 ? kPatches / 64 : 1;
   static constexpr int kItems = kThreads / 64 / kItemWaves;      // items of one workgroup
-  static_assert(kItemWaves <= kThreads / 64, "an item fits one workgroup");
 };
 
 template <int DT, int D, int B>
@@ -150,19 +152,19 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     const int64_t ph = (int64_t)(here ? page : 0) * kv.kv_heads + (have ? head : 0);
     uint8_t* const exps = (is_v ? kv.ve : kv.ke) + ph;
     const int had = *exps;
-    const int base = lp * B + 16 * tg;
+    const int base = lp * B + kPatch * tg;
     int i0 = lo - base, i1 = hi - base;
-    i0 = i0 < 0 ? 0 : (i0 > 16 ? 16 : i0);
-    i1 = i1 < 0 ? 0 : (i1 > 16 ? 16 : i1);
+    i0 = i0 < 0 ? 0 : (i0 > kPatch ? kPatch : i0);
+    i1 = i1 < 0 ? 0 : (i1 > kPatch ? kPatch : i1);
     const bool active = have && patch < SH::kPatches;
     if (!active) i0 = i1 = 0;
     auto row = [&](int i) { return (int64_t)(first + (base + i - past)) * stride + (int64_t)head * D; };
-    // more than two new tokens in the patch: all 16 places at once (those without a new token repeat
+    // more than two new tokens in the patch: all its places at once (those without a new token repeat
     // one that is, and are not stored); one or two, as in decoding: one after the other
     const bool many = i1 - i0 > 2;
     float amax = 0.0f;
     // Read once for the maximum and once more (from the caches) for the codes: kept in registers instead,
-    // 16 x 8 floats leave too few waves for the queries' copy in the same launch.
+    // they leave too few waves for the queries' copy in the same launch.
     auto four = [&](int i, float (*v)[8]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -173,7 +175,7 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     };
     if (many) {
 #pragma unroll 1
-      for (int i = 0; i < 16; i += 4) {
+      for (int i = 0; i < kPatch; i += 4) {
         float v[4][8];
         four(i, v);
 #pragma unroll
@@ -205,8 +207,8 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     const int shift = fresh ? 0 : had - b;
     if (patch == 0 && b != had) *exps = (uint8_t)b;
     const int64_t at = ph * (D * B);
-    uint8_t* const kc = kv.k + at + (int64_t)(16 * tg) * D + 8 * c;
-    uint8_t* const vc = kv.v + at + (int64_t)(8 * c) * B + 16 * tg;
+    uint8_t* const kc = kv.k + at + (int64_t)(kPatch * tg) * D + 8 * c;
+    uint8_t* const vc = kv.v + at + (int64_t)(8 * c) * B + kPatch * tg;
     // old tokens of the patch at the new scale
     if (shift < 0 && i0 > 0) {
       if (!is_v) {
@@ -216,16 +218,16 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
           *p = v2i{(int)rescale4((uint32_t)o[0], shift), (int)rescale4((uint32_t)o[1], shift)};
         }
       } else {
-        // 16 bytes of each feature, those past i0 kept
+        // 8 bytes of each feature, those past i0 kept
         for (int e = 0; e < 8; ++e) {
-          v4i o = *(const v4i*)(vc + e * B);
+          v2i o = *(const v2i*)(vc + e * B);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < kPatch / 4; ++w) {
             const int n = i0 - 4 * w;                             // old tokens in this word
             const uint32_t mask = n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
             o[w] = (int)((rescale4((uint32_t)o[w], shift) & mask) | ((uint32_t)o[w] & ~mask));
           }
-          *(v4i*)(vc + e * B) = o;
+          *(v2i*)(vc + e * B) = o;
         }
       }
     }
@@ -239,7 +241,7 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     if (many) {
       if (!is_v) {
 #pragma unroll 1
-        for (int i = 0; i < 16; i += 4) {
+        for (int i = 0; i < kPatch; i += 4) {
           float v[4][8];
           four(i, v);
 #pragma unroll
@@ -250,10 +252,10 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
           }
         }
       } else {
-        // 16 tokens of a feature together: 4 x 4 byte transpositions
-        uint32_t o[8][4];                          // [feature][four tokens]
+        // the tokens of a feature together: 4 x 4 byte transpositions
+        uint32_t o[8][kPatch / 4];                 // [feature][four tokens]
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < kPatch / 4; ++w) {
           float v[4][8];
           uint32_t q[4][2];
           four(4 * w, v);
@@ -269,10 +271,10 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
             o[4 * h + 3][w] = __builtin_amdgcn_perm(h23, h01, 0x07060302u);
           }
         }
-        if (i1 - i0 < 16) {
+        if (i1 - i0 < kPatch) {
           // bytes of places without a new token stay (the patch is this thread's alone)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < kPatch / 4; ++w) {
             uint32_t put = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) put |= 4 * w + j >= i0 && 4 * w + j < i1 ? 0xffu << (8 * j) : 0u;
@@ -281,7 +283,7 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) *(v4i*)(vc + e * B) = v4i{(int)o[e][0], (int)o[e][1], (int)o[e][2], (int)o[e][3]};
+        for (int e = 0; e < 8; ++e) *(v2i*)(vc + e * B) = v2i{(int)o[e][0], (int)o[e][1]};
       }
     } else {
       for (int i = i0; i < i1; ++i) {
@@ -301,10 +303,75 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
   }
 }
 
+// One new token of a sequence: D / 8 lanes hold a kv head's keys or values, 8 features each, and
+// decide its scale among themselves.  `slot`: this lane's place among the sequence's heads x features.
+template <int DT, int D, int B>
+__device__ void append_token(const AppendArgs& a, int s, int first, int pos, int slot) {
+  constexpr int kCols = D / 8;
+  const KvView& kv = a.kv;
+  const int item = slot / kCols, c = slot % kCols;
+  const bool is_v = item >= kv.kv_heads, have = item < 2 * kv.kv_heads;
+  const int head = have ? (is_v ? item - kv.kv_heads : item) : 0;
+  const int lp = pos / B, off = pos % B;
+  const int page = lp < kv.max_pages ? kv.table[(int64_t)s * kv.max_pages + lp] : -1;
+  const bool here = page >= 0 && page < kv.num_pages;
+  const int64_t ph = (int64_t)(here ? page : 0) * kv.kv_heads + head;
+  uint8_t* const exps = (is_v ? kv.ve : kv.ke) + ph;
+  const int had = *exps;
+  float v[8];
+  if (is_v) load8<DT>(a.v, (int64_t)first * a.v_stride + (int64_t)head * D + 8 * c, v);
+  else load_rotated<DT>(a, a.k, (int64_t)first * a.k_stride + (int64_t)head * D, c, pos, v);
+  float amax = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  // over the head's 8, 16 or 32 lanes (bit patterns of non-negative floats order as integers)
+  int am = __float_as_int(amax);
+  auto up = [](int x, int y) { return x > y ? x : y; };
+  am = up(am, __builtin_amdgcn_update_dpp(0, am, 0xB1, 0xF, 0xF, false));
+  am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x4E, 0xF, 0xF, false));
+  am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x141, 0xF, 0xF, false));
+  if constexpr (kCols >= 16) am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x140, 0xF, 0xF, false));
+  if constexpr (kCols >= 32) am = up(am, __shfl_xor(am, 16));
+  if (!have || !here) return;
+  const bool fresh = off == 0;
+  const int want = exponent_byte(__int_as_float(am));
+  const int b = fresh ? want : (had > want ? had : want);
+  const int shift = fresh ? 0 : had - b;
+  if (c == 0 && b != had) *exps = (uint8_t)b;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], 127 - b);
+  const uint32_t q0 = pack4_e4m3(v[0], v[1], v[2], v[3]), q1 = pack4_e4m3(v[4], v[5], v[6], v[7]);
+  const int64_t at = ph * (D * B);
+  if (!is_v) {
+    uint8_t* const codes = kv.k + at + 8 * c;
+    if (shift < 0)
+#pragma unroll 8
+      for (int i = 0; i < off; ++i) {
+        v2i* p = (v2i*)(codes + i * D);
+        const v2i o = *p;
+        *p = v2i{(int)rescale4((uint32_t)o[0], shift), (int)rescale4((uint32_t)o[1], shift)};
+      }
+    *(v2i*)(codes + off * D) = v2i{(int)q0, (int)q1};
+  } else {
+    uint8_t* const codes = kv.v + at + (int64_t)(8 * c) * B;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint8_t* const row = codes + e * B;
+      if (shift < 0)
+        for (int i = 0; i < off; i += 4) {
+          uint32_t* p = (uint32_t*)(row + i);
+          const uint32_t mask = off - i >= 4 ? 0xffffffffu : (1u << (8 * (off - i))) - 1u;
+          *p = (rescale4(*p, shift) & mask) | (*p & ~mask);
+        }
+      row[off] = (uint8_t)((e < 4 ? q0 : q1) >> (8 * (e & 3)));
+    }
+  }
+}
+
 // The queries of one sequence: one token, 8 features (with pairs (i, i + r): both groups of 8 of a
 // pair) and `span` heads per thread, which share their cosines and sines.
 template <int DT, int D>
-__device__ void rotate_queries(const AppendArgs& a, int s, int block, int blocks, int span) {
+__device__ void rotate_queries(const AppendArgs& a, int s, int block, int blocks, int span, int threads) {
   const KvView& kv = a.kv;
   int end = kv.q_start[s + 1], first = kv.q_start[s];
   end = end < 0 ? 0 : (end > kv.tokens ? kv.tokens : end);
@@ -314,7 +381,7 @@ __device__ void rotate_queries(const AppendArgs& a, int s, int block, int blocks
   const int units = D / 8 - pairs, spans = (a.heads + span - 1) / span;
   const int per = units * spans;
   const int64_t all = (int64_t)(end - first) * per;
-  for (int64_t i = (int64_t)block * kThreads + threadIdx.x; i < all; i += (int64_t)blocks * kThreads) {
+  for (int64_t i = (int64_t)block * threads + threadIdx.x; i < all; i += (int64_t)blocks * threads) {
     const int t = (int)(i / per), r = (int)(i - (int64_t)t * per);
     const int h0 = r / units * span, u = r % units;
     const bool pair = u < pairs;
@@ -346,19 +413,34 @@ __device__ void rotate_queries(const AppendArgs& a, int s, int block, int blocks
 }
 
 template <int DT, int D, int B>
-__global__ __launch_bounds__(kThreads, 4) void k_kv_append(const AppendArgs a, int kv_blocks, int groups, int q_blocks,
-                                                            int span) {
-  __shared__ float red[kThreads / 64];
+__global__ __launch_bounds__((Shape<DT, D, B>::kThreads), 4) void k_kv_append(const AppendArgs a, int kv_blocks, int groups, int q_blocks,
+                                                                                        int span, int token_blocks) {
+  using SH = Shape<DT, D, B>;
+  __shared__ float red[SH::kThreads / 64];
   // the pages' workgroups (few bytes, several round trips) spread evenly among the queries' (a stream):
   // workgroup i is number floor(i kv / all) of the pages' where that number grows behind it
   const int64_t all = gridDim.x, i = blockIdx.x;
   const int before = (int)(i * kv_blocks / all), after = (int)((i + 1) * kv_blocks / all);
   if (after > before) {
-    const int b = before / groups;
-    append_pages<DT, D, B>(a, b / a.reach, b % a.reach, before % groups, red);
+    if (token_blocks > 0) {
+      // one new token a sequence is expected; a sequence with another number takes its pages here too
+      const int s = before / token_blocks, part = before % token_blocks;
+      int end = a.kv.q_start[s + 1], first = a.kv.q_start[s];
+      end = end < 0 ? 0 : (end > a.kv.tokens ? a.kv.tokens : end);
+      first = first < 0 ? 0 : (first > end ? end : first);
+      const int pos = a.kv.kv_len[s] - 1;
+      if (end - first == 1) {
+        if (pos >= 0) append_token<DT, D, B>(a, s, first, pos, part * SH::kThreads + threadIdx.x);
+      } else {
+        for (int g = part; g < groups; g += token_blocks) append_pages<DT, D, B>(a, s, 0, g, red);
+      }
+    } else {
+      const int b = before / groups;
+      append_pages<DT, D, B>(a, b / a.reach, b % a.reach, before % groups, red);
+    }
   } else {
     const int b = (int)i - before;
-    rotate_queries<DT, D>(a, b / q_blocks, b % q_blocks, q_blocks, span);
+    rotate_queries<DT, D>(a, b / q_blocks, b % q_blocks, q_blocks, span, SH::kThreads);
   }
 }
 
@@ -366,19 +448,22 @@ template <int DT, int D, int B>
 hipError_t launch_shape(const AppendArgs& a, hipStream_t st) {
   using SH = Shape<DT, D, B>;
   const int64_t groups = (2 * a.kv.kv_heads + SH::kItems - 1) / SH::kItems;
-  const int64_t kv_blocks = (int64_t)a.kv.seqs * a.reach * groups;
+  // one new token each: lanes by head and features instead of patches, of which it would fill one lane
+  // in B / kPatch
+  const int64_t token_blocks = a.max_q == 1 ? ((int64_t)2 * a.kv.kv_heads * (D / 8) + SH::kThreads - 1) / SH::kThreads : 0;
+  const int64_t kv_blocks = token_blocks > 0 ? a.kv.seqs * token_blocks : (int64_t)a.kv.seqs * a.reach * groups;
   int64_t q_blocks = 0;
   // heads of a thread: one where there are few tokens (latency), eight that share their angles elsewhere
   const int span = (int64_t)a.max_q * a.kv.seqs >= 1024 ? 8 : 1;
   if (a.q) {
     const int64_t units = D / 8 - (a.interleaved ? 0 : a.rot >> 4), spans = (a.heads + span - 1) / span;
-    q_blocks = ((int64_t)a.max_q * units * spans + kThreads - 1) / kThreads;
+    q_blocks = ((int64_t)a.max_q * units * spans + SH::kThreads - 1) / SH::kThreads;
     const int64_t most = ((int64_t)1 << 30) / a.kv.seqs;
     q_blocks = q_blocks > most ? most : q_blocks;
   }
   if (kv_blocks + q_blocks * a.kv.seqs > ((int64_t)1 << 31) - 1) return hipErrorInvalidValue;
-  k_kv_append<DT, D, B><<<(unsigned)(kv_blocks + q_blocks * a.kv.seqs), kThreads, 0, st>>>(
-      a, (int)kv_blocks, (int)groups, q_blocks > 0 ? (int)q_blocks : 1, span);
+  k_kv_append<DT, D, B><<<(unsigned)(kv_blocks + q_blocks * a.kv.seqs), SH::kThreads, 0, st>>>(
+      a, (int)kv_blocks, (int)groups, q_blocks > 0 ? (int)q_blocks : 1, span, (int)token_blocks);
   return hipGetLastError();
 }
 
