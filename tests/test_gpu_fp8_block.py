@@ -131,3 +131,24 @@ def test_empty_batch_and_refusals():
         q8.q8_quantize_weight_block(torch.zeros(4, 24, device=DEV))
     with pytest.raises(_lib.Q8Error):
         q8.q8_linear_fp8_block(torch.zeros(64, 128, device=DEV), wq, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 40, 300, 2100])
+@pytest.mark.parametrize("K", [128, 144, 400])
+def test_nan_codes_stay_in_their_row_and_column(M, K):
+    """A K that ends inside a block of 128: what lies past a row in memory is another row's."""
+    N = 1000
+    x, w, _ = inputs(11, M, N, K, BF)
+    wq, ws = q8.q8_quantize_weight_block(w.to(DEV))
+    xq, xs = q8.q8_quantize_act_block(x.to(DEV))
+    clean = q8.q8_gemm_fp8_block(xq, xs, wq, ws)
+    nan_w = [1, 500, N - 1]
+    wq[nan_w] = 0x7F
+    y = q8.q8_gemm_fp8_block(xq, xs, wq, ws)
+    keep = [n for n in range(N) if n not in nan_w]
+    assert torch.equal(y[:, keep], clean[:, keep]) and y[:, nan_w].isnan().all()
+    if M > 2:
+        xq[1] = 0x7F
+        y = q8.q8_gemm_fp8_block(xq, xs, wq, ws)
+        rows = [m for m in range(M) if m != 1]
+        assert torch.equal(y[rows][:, keep], clean[rows][:, keep]) and y[1].isnan().all()

@@ -99,7 +99,9 @@ __global__ __launch_bounds__(kThreads) void k_quant_weight_block(const void* __r
 // needs two, and four times the registers for the sums: 243 against 233 us at
 // 4096 x 4096 x 14336 in the kernel trace).
 // One stage is one block, 128 bytes of K of every tile row, filled by LDS DMA
-// with the block's activation scales of the tile beside it.
+// with the block's activation scales of the tile beside it.  The last block
+// goes the same way and is cut at K in registers (a pass of its own through
+// registers: 11.0 against 9.9 us at 333 x 1000 x 2064).
 constexpr int kBK = kScaleBlock;
 constexpr int kXcds = 8;
 constexpr int kGroupM = 4;       // tile rows that share weight tiles in L2
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     m0 = (first + (b - g * per) % size) * BM;
     n0 = (b - g * per) / size * BN;
   }
-  const int groups = (K + kBK - 1) / kBK, full = K / kBK;
+  const int groups = (K + kBK - 1) / kBK;
 
   // DMA: instruction d of this wave fills rows 8 (d kWaves + wave) .. + 7 of the stage (activation
   // rows first); lane l lands at row l / 8, chunk l % 8, and fetches the chunk that belongs there.
@@ -197,20 +199,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     }
     dma4_buf(ress, offs, (uint32_t)j * (uint32_t)M * 4u, ssc + slot * BM + (wave % TL::kScales) * 64);
   };
-  // a last block that K ends inside: through registers, zeros past K
-  auto tail = [&](int j) {
-    uint8_t* const st = smem + (j % NST) * TL::kStage;
-    for (int c = tid; c < (BM + BN) * 8; c += TL::kThreads) {
-      const int r = c >> 3, k = j * kBK + (c & 7) * 16;
-      int row = r < BM ? m0 + r : n0 + r - BM;
-      const int most = r < BM ? M - 1 : N - 1;
-      row = row < most ? row : most;
-      const uint8_t* p = (r < BM ? xq : wq) + (int64_t)row * K + k;
-      *(v4i*)(st + r * kBK + (((c & 7) ^ swz_key(r)) << 4)) = k < K ? *(const v4i*)p : v4i{0, 0, 0, 0};
-    }
-    if (tid < BM) ssc[(j % NST) * BM + tid] = x_scale[(int64_t)j * M + (m0 + tid < M ? m0 + tid : M - 1)];
-  };
-
   v4f acc[AF][BF];
 #pragma unroll
   for (int i = 0; i < AF; ++i)
@@ -250,11 +238,27 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[i][f][r] = __builtin_fmaf(s, p[r], acc[i][f][r]);
   };
-  // Block j; `next` (uniform) runs once this wave has read all of it, and returns whether the
-  // registers are to be filled from the next slot.
+  // K may end inside the last block, whose LDS rows then go on with what follows in memory, another
+  // row's codes: they are cleared on both sides (a NaN among them stays in its own row)
+  const int chunks = (K - (groups - 1) * kBK) >> 4, keep_lo = lg < chunks ? -1 : 0, keep_hi = lg + 4 < chunks ? -1 : 0;
+  auto cut = [&](v8i& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] &= keep_lo;
+      v[4 + e] &= keep_hi;
+    }
+  };
+  // A block; `next` (uniform) runs once this wave has read all of it and returns the slot that the
+  // registers are filled from.  The last block (not NEXT) fills none and is cut at K.
   auto block = [&](int slot, auto NEXT, auto&& next) {
     constexpr bool more = decltype(NEXT)::value;
     sw = swn;
+    if (!more) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) cut(fa[h]);
+#pragma unroll
+      for (int f = 0; f < BF; ++f) cut(fb[f]);
+    }
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       v4f p[BF];
@@ -263,6 +267,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
       const float s = sx[h] * sw;
       __builtin_amdgcn_sched_barrier(0);
       load_a(slot, h, H + h);
+      if (!more) cut(fa[h]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int f = 0; f < BF; ++f) add(h, f, s, p[f]);
@@ -309,40 +314,29 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
   };
 
   // All NST buffers are filled ahead, a buffer again as soon as every wave has read its block.  Past
-  // the last full block the DMA repeats it, into buffers nobody reads, so that the loop has no
+  // the last block the DMA repeats it, into buffers nobody reads, so that the loop has no
   // branch and the number of loads in flight is always the same.
   auto arrived = [&] {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (TL::kLoads + 1)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  auto clamped = [&](int b) { return b < full ? b : full - 1; };
-  int j = 0;
-  if (full > 0) {
+  auto clamped = [&](int b) { return b < groups ? b : groups - 1; };
 #pragma unroll
-    for (int b = 0; b < NST - 1; ++b) dma(clamped(b), b);
-    arrived();
-    dma(clamped(NST - 1), NST - 1);
-    load_all(0, 0);
-    for (; j + 1 < full; ++j)
-      block(j % NST, std::true_type{}, [&] {
-        __builtin_amdgcn_s_waitcnt(kLgkmcnt0);          // this wave's reads of block j are done
-        arrived();
-        dma(clamped(j + NST), j % NST);
-        swn = wsc[j + 1];
-        return (j + 1) % NST;
-      });
-  }
-  for (; j < groups; ++j) {
-    if (j >= full) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      tail(j);
-      __syncthreads();
-      load_all(j % NST, j);
-    }
-    block(j % NST, std::false_type{}, [] { return 0; });
-  }
+  for (int b = 0; b < NST - 1; ++b) dma(clamped(b), b);
+  arrived();
+  dma(clamped(NST - 1), NST - 1);
+  load_all(0, 0);
+  int j = 0;
+  for (; j + 1 < groups; ++j)
+    block(j % NST, std::true_type{}, [&] {
+      __builtin_amdgcn_s_waitcnt(kLgkmcnt0);          // this wave's reads of block j are done
+      arrived();
+      dma(clamped(j + NST), j % NST);
+      swn = wsc[j + 1];
+      return (j + 1) % NST;
+    });
+  block(j % NST, std::false_type{}, [] { return 0; });
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // repeated blocks still on their way
 
   // epilogue: one 16-row slab of a wave at a time through padded LDS, back row-contiguous, 8 columns a lane
