@@ -790,10 +790,11 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
   const int64_t groups = pairs * p.blocks;
   const int64_t step = 512;
   // Splits to fill the chip, none where the sequences and heads do it alone (64 sequences, 8 kv heads,
-  // up to 4099 keys: 74 us whole, 77 + 5 in 1024-key shares), but none longer than 8192 keys either,
-  // so that one long sequence among many does not hold up the rest.
+  // up to 4099 keys: 74 us whole, 77 + 5 in 1024-key shares).  Few rows: none longer than 8192 keys
+  // either, so that one long sequence among many does not hold up the rest; many rows are cut by
+  // rows, and a split would only add their partial sums' traffic.
   int64_t want = p.per == kSmallRows ? (groups >= 512 ? 1 : 1024 / groups) : groups >= 192 ? 1 : 512 / groups;
-  want = want < keys / 8192 ? keys / 8192 : want;
+  if (p.per == kSmallRows && want < keys / 8192) want = keys / 8192;
   const int64_t most = (keys + step - 1) / step;
   want = want > most ? most : want;
   want = want > kMaxSplits ? kMaxSplits : want;
@@ -804,7 +805,6 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
   if (p.splits < 1) p.splits = 1;
   p.chunk = (int)c;
   const int64_t most_blocks = ((int64_t)1 << 30) / (pairs * p.splits);
-  if (p.per == kSmallRows && p.blocks > 65535 / seqs) p.blocks = 65535 / seqs;
   if (p.blocks > most_blocks) p.blocks = most_blocks;
   if (p.blocks < 1) p.blocks = 1;
   return p;
