@@ -144,10 +144,11 @@ struct Tile {
   static constexpr int kStage = (BM + BN) * kBK;
   static constexpr int kLoads = (BM + BN) / 8 / kWaves;    // 1 KB DMAs (8 rows) of a wave and stage
   static constexpr int kScales = BM / 64;                  // 64-row DMAs of activation scales of a stage
-  static constexpr int kScaleBytes = BM * 4;
+  static constexpr bool kAhead = AF * BF <= 8;             // a whole block ahead in registers
+  static constexpr int kScaleBytes = (BM + (kAhead ? 64 : 0)) * 4;
   static constexpr int kPitch = TN * 4 + 16;               // epilogue staging of one 16-row slab
   static constexpr int kLds = NST * (kStage + kScaleBytes);
-  static_assert((BM + BN) / 8 % kWaves == 0 && BM % 64 == 0 && kScales <= kWaves, "DMA split");
+  static_assert((BM + BN) / 8 % kWaves == 0 && BM % 64 == 0 && kScales + kAhead <= kWaves, "DMA split");
   static_assert(kWaves * 16 * kPitch <= kLds, "the epilogue's staging fits");
 };
 
@@ -185,19 +186,29 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
   const int r0 = wave * 8 + (lane >> 3);
   const uint32_t chunk = (uint32_t)((lane & 7) ^ swz_key(r0)) << 4;
   const uint32_t offx = (uint32_t)(m0 + r0) * (uint32_t)K + chunk, offw = (uint32_t)(n0 + r0) * (uint32_t)K + chunk;
-  const uint32_t offs = (uint32_t)(m0 + (wave % TL::kScales) * 64 + lane) * 4u;
+  // scales: 64 rows' of the activations, or (kAhead) the one of the tile's weight rows 64 times
+  const int part = wave % (TL::kScales + TL::kAhead);
+  const bool wpart = TL::kAhead && part == TL::kScales;
+  const uint32_t offs = wpart ? (uint32_t)(n0 / kScaleBlock) * (uint32_t)groups * 4u : (uint32_t)(m0 + part * 64 + lane) * 4u;
   const v4i resx = buffer_words(xq, (uint32_t)M * (uint32_t)K), resw = buffer_words(wq, (uint32_t)N * (uint32_t)K);
-  const v4i ress = buffer_words(x_scale, (uint32_t)M * (uint32_t)groups * 4u);
-  auto dma = [&](int j, int slot) {
-    uint8_t* const st = smem + slot * TL::kStage + wave * 1024;
-#pragma unroll
-    for (int d = 0; d < TL::kLoads; ++d) {
-      const bool w = d * kStep >= BM;
-      // the row step belongs to the per-lane offset: the range check takes the scalar one off the size
-      const uint32_t step = (uint32_t)(w ? d * kStep - BM : d * kStep) * (uint32_t)K;
-      dma16_buf(w ? resw : resx, (w ? offw : offx) + step, (uint32_t)j * kBK, st + d * TL::kWaves * 1024);
+  const v4i ress = buffer_words(wpart ? w_scale : x_scale,
+                                (wpart ? (uint32_t)((N + kScaleBlock - 1) / kScaleBlock) : (uint32_t)M) * (uint32_t)groups * 4u);
+  const uint32_t steps = (wpart ? 1u : (uint32_t)M) * 4u;
+  // instruction d of block j's kLoads + 1
+  auto dma_one = [&](int j, int slot, int d) {
+    if (d == TL::kLoads) {
+      dma4_buf(ress, offs, (uint32_t)j * steps, ssc + slot * (TL::kScaleBytes / 4) + part * 64);
+      return;
     }
-    dma4_buf(ress, offs, (uint32_t)j * (uint32_t)M * 4u, ssc + slot * BM + (wave % TL::kScales) * 64);
+    const bool w = d * kStep >= BM;
+    // the row step belongs to the per-lane offset: the range check takes the scalar one off the size
+    const uint32_t step = (uint32_t)(w ? d * kStep - BM : d * kStep) * (uint32_t)K;
+    dma16_buf(w ? resw : resx, (w ? offw : offx) + step, (uint32_t)j * kBK,
+              smem + slot * TL::kStage + wave * 1024 + d * TL::kWaves * 1024);
+  };
+  auto dma = [&](int j, int slot) {
+#pragma unroll
+    for (int d = 0; d <= TL::kLoads; ++d) dma_one(j, slot, d);
   };
   v4f acc[AF][BF];
 #pragma unroll
@@ -217,22 +228,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
     const v4i a = *(const v4i*)(rows + lo), b = *(const v4i*)(rows + lo2);
     return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   };
-  // the wave's columns lie in one block of 128 weight rows
-  const int nw = n0 + wn * TL::TN < N ? n0 + wn * TL::TN : N - 1;
-  const float* const wsc = w_scale + (int64_t)(nw / kScaleBlock) * groups;
-
-  // The block's weight fragments and half of its activation fragments are in registers; a fragment's
-  // registers are loaded again as soon as its last MFMA is issued, so LDS reads run all the time and a
-  // wave leaves the barrier with the second half of a block still to multiply.
-  float sw, swn, sx[H];
-  v8i fb[BF], fa[H];
-  auto load_b = [&](int slot, int f) { fb[f] = frag(sw_rows + slot * TL::kStage + f * 16 * kBK); };
-  auto load_a = [&](int slot, int h, int i) {
-    fa[h] = frag(sx_rows + slot * TL::kStage + i * 16 * kBK);
-    sx[h] = ssc[slot * BM + wm * TL::TM + 16 * i + lr];
-  };
-  auto mma = [&](int f, int h) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[f], fa[h], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+  auto mma = [&](const v8i& w, const v8i& x) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
   };
   auto add = [&](int i, int f, float s, const v4f p) {
 #pragma unroll
@@ -248,71 +245,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
       v[4 + e] &= keep_hi;
     }
   };
-  // A block; `next` (uniform) runs once this wave has read all of it and returns the slot that the
-  // registers are filled from.  The last block (not NEXT) fills none and is cut at K.
-  auto block = [&](int slot, auto NEXT, auto&& next) {
-    constexpr bool more = decltype(NEXT)::value;
-    sw = swn;
-    if (!more) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) cut(fa[h]);
-#pragma unroll
-      for (int f = 0; f < BF; ++f) cut(fb[f]);
-    }
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      v4f p[BF];
-#pragma unroll
-      for (int f = 0; f < BF; ++f) p[f] = mma(f, h);
-      const float s = sx[h] * sw;
-      __builtin_amdgcn_sched_barrier(0);
-      load_a(slot, h, H + h);
-      if (!more) cut(fa[h]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int f = 0; f < BF; ++f) add(h, f, s, p[f]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const int to = next();
-    float s[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h) s[h] = sx[h] * sw;
-#pragma unroll
-    for (int d = 0; d < (H > BF ? H : BF); ++d) {
-      v4f p[H], q[BF];
-      if (d < BF) {
-#pragma unroll
-        for (int h = d; h < H; ++h) p[h] = mma(d, h);
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) load_b(to, d);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (d < H) {
-#pragma unroll
-        for (int f = d + 1; f < BF; ++f) q[f] = mma(f, d);
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) load_a(to, d, d);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (d < BF) {
-#pragma unroll
-        for (int h = d; h < H; ++h) add(H + h, d, s[h], p[h]);
-      }
-      if (d < H) {
-#pragma unroll
-        for (int f = d + 1; f < BF; ++f) add(H + d, f, s[d], q[f]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  auto load_all = [&](int slot, int j) {
-#pragma unroll
-    for (int f = 0; f < BF; ++f) load_b(slot, f);
-#pragma unroll
-    for (int h = 0; h < H; ++h) load_a(slot, h, h);
-    swn = wsc[j];
-  };
-
   // All NST buffers are filled ahead, a buffer again as soon as every wave has read its block.  Past
   // the last block the DMA repeats it, into buffers nobody reads, so that the loop has no
   // branch and the number of loads in flight is always the same.
@@ -326,17 +258,169 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
   for (int b = 0; b < NST - 1; ++b) dma(clamped(b), b);
   arrived();
   dma(clamped(NST - 1), NST - 1);
-  load_all(0, 0);
-  int j = 0;
-  for (; j + 1 < groups; ++j)
-    block(j % NST, std::true_type{}, [&] {
-      __builtin_amdgcn_s_waitcnt(kLgkmcnt0);          // this wave's reads of block j are done
+  if constexpr (TL::kAhead) {
+    // Small wave tiles: the next block's operands go from LDS into a second set of registers and the
+    // DMA of a later one is requested while this block's products run, a few requests after each
+    // (all of them before the products: 70.9 against 55.9 us for 128 x 128 tiles at 512 x 2048 x
+    // 16384, where nothing but this loop counts).
+    v8i fa[2][AF], fb[2][BF];
+    float sx[2][AF], sw[2];
+    constexpr int kReads = AF + BF + 1, kProducts = AF * BF, kOps = kReads + TL::kLoads + 1;
+    // read r of a block's kReads: its scales, a weight or an activation fragment
+    auto read = [&](int slot, auto SET, int r) {
+      constexpr int t = decltype(SET)::value;
+      const float* const sc = ssc + slot * (TL::kScaleBytes / 4);
+      if (r == 0) {
+#pragma unroll
+        for (int i = 0; i < AF; ++i) sx[t][i] = sc[wm * TL::TM + 16 * i + lr];
+        sw[t] = sc[BM];
+      } else if (r <= BF) {
+        fb[t][r - 1] = frag(sw_rows + slot * TL::kStage + (r - 1) * 16 * kBK);
+      } else {
+        fa[t][r - 1 - BF] = frag(sx_rows + slot * TL::kStage + (r - 1 - BF) * 16 * kBK);
+      }
+    };
+    // The block of SET multiplied; after product c, `between(c)`.
+    auto multiply = [&](auto SET, auto&& between) {
+      constexpr int t = decltype(SET)::value;
+      v4f p[AF][BF];
+#pragma unroll
+      for (int c = 0; c < kProducts; ++c) {
+        p[c / BF][c % BF] = mma(fb[t][c % BF], fa[t][c / BF]);
+        __builtin_amdgcn_sched_barrier(0);
+        between(c);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int c = 0; c < kProducts; ++c) add(c / BF, c % BF, sx[t][c / BF] * sw[t], p[c / BF][c % BF]);
+    };
+    auto last = [&](auto SET) {
+      constexpr int t = decltype(SET)::value;
+#pragma unroll
+      for (int i = 0; i < AF; ++i) cut(fa[t][i]);
+#pragma unroll
+      for (int f = 0; f < BF; ++f) cut(fb[t][f]);
+      multiply(SET, [](int) {});
+    };
+    constexpr std::integral_constant<int, 0> even;
+    constexpr std::integral_constant<int, 1> odd;
+    auto step = [&](int j, auto SET, auto NEXT) {
+      __builtin_amdgcn_s_waitcnt(kLgkmcnt0);            // this wave's reads of block j are done
       arrived();
-      dma(clamped(j + NST), j % NST);
-      swn = wsc[j + 1];
-      return (j + 1) % NST;
-    });
-  block(j % NST, std::false_type{}, [] { return 0; });
+      const int from = (j + 1) % NST, to = j % NST, b = clamped(j + NST);
+      multiply(SET, [&](int c) {
+#pragma unroll
+        for (int o = c * kOps / kProducts; o < (c + 1) * kOps / kProducts; ++o) {
+          if (o < kReads) read(from, NEXT, o);
+          else dma_one(b, to, o - kReads);
+        }
+      });
+    };
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(0, even, r);
+    int j = 0;
+    for (; j + 2 < groups; j += 2) {
+      step(j, even, odd);
+      step(j + 1, odd, even);
+    }
+    if (j + 1 < groups) {
+      step(j, even, odd);
+      last(odd);
+    } else {
+      last(even);
+    }
+  } else {
+    // the wave's columns lie in one block of 128 weight rows
+    const int nw = n0 + wn * TL::TN < N ? n0 + wn * TL::TN : N - 1;
+    const float* const wsc = w_scale + (int64_t)(nw / kScaleBlock) * groups;
+
+    // The block's weight fragments and half of its activation fragments are in registers; a fragment's
+    // registers are loaded again as soon as its last MFMA is issued, so LDS reads run all the time and a
+    // wave leaves the barrier with the second half of a block still to multiply.
+    float sw, swn, sx[H];
+    v8i fb[BF], fa[H];
+    auto load_b = [&](int slot, int f) { fb[f] = frag(sw_rows + slot * TL::kStage + f * 16 * kBK); };
+    auto load_a = [&](int slot, int h, int i) {
+      fa[h] = frag(sx_rows + slot * TL::kStage + i * 16 * kBK);
+      sx[h] = ssc[slot * (TL::kScaleBytes / 4) + wm * TL::TM + 16 * i + lr];
+    };
+    // A block; `next` (uniform) runs once this wave has read all of it and returns the slot that the
+    // registers are filled from.  The last block (not NEXT) fills none and is cut at K.
+    auto block = [&](int slot, auto NEXT, auto&& next) {
+      constexpr bool more = decltype(NEXT)::value;
+      sw = swn;
+      if (!more) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) cut(fa[h]);
+#pragma unroll
+        for (int f = 0; f < BF; ++f) cut(fb[f]);
+      }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        v4f p[BF];
+#pragma unroll
+        for (int f = 0; f < BF; ++f) p[f] = mma(fb[f], fa[h]);
+        const float s = sx[h] * sw;
+        __builtin_amdgcn_sched_barrier(0);
+        load_a(slot, h, H + h);
+        if (!more) cut(fa[h]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < BF; ++f) add(h, f, s, p[f]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const int to = next();
+      float s[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) s[h] = sx[h] * sw;
+#pragma unroll
+      for (int d = 0; d < (H > BF ? H : BF); ++d) {
+        v4f p[H], q[BF];
+        if (d < BF) {
+#pragma unroll
+          for (int h = d; h < H; ++h) p[h] = mma(fb[d], fa[h]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (more) load_b(to, d);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (d < H) {
+#pragma unroll
+          for (int f = d + 1; f < BF; ++f) q[f] = mma(fb[f], fa[d]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (more) load_a(to, d, d);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (d < BF) {
+#pragma unroll
+          for (int h = d; h < H; ++h) add(H + h, d, s[h], p[h]);
+        }
+        if (d < H) {
+#pragma unroll
+          for (int f = d + 1; f < BF; ++f) add(H + d, f, s[d], q[f]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto load_all = [&](int slot, int j) {
+#pragma unroll
+      for (int f = 0; f < BF; ++f) load_b(slot, f);
+#pragma unroll
+      for (int h = 0; h < H; ++h) load_a(slot, h, h);
+      swn = wsc[j];
+    };
+
+    load_all(0, 0);
+    int j = 0;
+    for (; j + 1 < groups; ++j)
+      block(j % NST, std::true_type{}, [&] {
+        __builtin_amdgcn_s_waitcnt(kLgkmcnt0);          // this wave's reads of block j are done
+        arrived();
+        dma(clamped(j + NST), j % NST);
+        swn = wsc[j + 1];
+        return (j + 1) % NST;
+      });
+    block(j % NST, std::false_type{}, [] { return 0; });
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // repeated blocks still on their way
 
   // epilogue: one 16-row slab of a wave at a time through padded LDS, back row-contiguous, 8 columns a lane
@@ -373,74 +457,65 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_gemm_tiles(
 }
 
 // ---------------------------------------------------------------- few tokens
-// Decode-shaped: a workgroup owns 16 NF weight rows, its 4 waves take every
-// fourth block of K (v_mfma_f32_16x16x128_f8f6f4: one block an instruction),
-// AHEAD blocks at a time, all of whose weights and activations are requested
-// before the first is used, straight into registers, and join through LDS.  MF
-// fragments of 16 tokens share a weight operand, NF fragments of 16 weight rows
-// an activation operand.
+// Decode-shaped: a workgroup owns 16 weight rows, its 4 waves take every fourth
+// block of K (v_mfma_f32_16x16x128_f8f6f4: one block an instruction), AHEAD
+// blocks at a time, all of whose weights and activations are requested before
+// the first is used, straight into registers, and join through LDS.  MF
+// fragments of 16 tokens share a weight operand.
 constexpr int kGemvWaves = kThreads / 64;
 
-// Joins the waves' sums of a 16 NF x 16 MF tile and stores them.
-template <int MF, int NF, int YDT>
-__device__ __forceinline__ void gemv_store(v4f (&acc)[NF][MF], v4f (*part)[NF * MF][64], int wave, int lane, int M, int N,
-                                           int n0, const float* bias, void* y) {
+// Joins the waves' sums of a 16 x 16 MF tile and stores them.
+template <int MF, int YDT>
+__device__ __forceinline__ void gemv_store(v4f (&acc)[MF], v4f (*part)[MF][64], int wave, int lane, int M, int N, int n0,
+                                           const float* bias, void* y) {
 #pragma unroll
-  for (int i = 0; i < NF; ++i)
-#pragma unroll
-    for (int f = 0; f < MF; ++f) part[wave][i * MF + f][lane] = acc[i][f];
+  for (int f = 0; f < MF; ++f) part[wave][f][lane] = acc[f];
   __syncthreads();
   const int lr = lane & 15, lg = lane >> 4;
-  for (int q = wave; q < NF * MF; q += kGemvWaves) {
-    const int m = 16 * (q % MF) + lr, n4 = n0 + 16 * (q / MF) + 4 * lg;
-    if (m >= M) continue;
-    v4f t = part[0][q][lane];
+  const int m = 16 * wave + lr, n4 = n0 + 4 * lg;
+  if (wave >= MF || m >= M) return;
+  v4f t = part[0][wave][lane];
 #pragma unroll
-    for (int w = 1; w < kGemvWaves; ++w) t += part[w][q][lane];
+  for (int w = 1; w < kGemvWaves; ++w) t += part[w][wave][lane];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n4 + r < N) store_out<YDT>(y, (int64_t)m * N + n4 + r, t[r] + (bias ? bias[n4 + r] : 0.0f));
-  }
+  for (int r = 0; r < 4; ++r)
+    if (n4 + r < N) store_out<YDT>(y, (int64_t)m * N + n4 + r, t[r] + (bias ? bias[n4 + r] : 0.0f));
 }
 
 __device__ __forceinline__ v8i join8(const v4i a, const v4i b) {
   return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-template <int MF, int NF, int AHEAD, int YDT>
+template <int MF, int AHEAD, int YDT>
 __global__ __launch_bounds__(kThreads) void k_gemv_block(const uint8_t* __restrict__ xq, const float* __restrict__ x_scale,
                                                          int M, int K, const uint8_t* __restrict__ wq,
                                                          const float* __restrict__ w_scale, int N,
                                                          const float* __restrict__ bias, void* __restrict__ y) {
-  __shared__ v4f part[kGemvWaves][NF * MF][64];
+  static_assert(MF <= kGemvWaves, "a wave a fragment at the join");
+  __shared__ v4f part[kGemvWaves][MF][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NF;
+  const int n0 = blockIdx.x * 16;
   const int groups = (K + kScaleBlock - 1) / kScaleBlock;
   // rows past N and tokens past M read the last ones and are not stored
-  const uint8_t *wp[NF], *xp[MF];
-  const float *ws[NF], *xs[MF];
-#pragma unroll
-  for (int i = 0; i < NF; ++i) {
-    const int n = n0 + 16 * i + lr < N ? n0 + 16 * i + lr : N - 1;
-    wp[i] = wq + (int64_t)n * K + 32 * lg;
-    ws[i] = w_scale + (int64_t)(n / kScaleBlock) * groups;
-  }
+  const int n = n0 + lr < N ? n0 + lr : N - 1;
+  const uint8_t* const wp = wq + (int64_t)n * K + 32 * lg;
+  const float* const ws = w_scale + (int64_t)(n0 / kScaleBlock) * groups;
+  const uint8_t* xp[MF];
+  const float* xs[MF];
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
     const int m = 16 * f + lr < M ? 16 * f + lr : M - 1;
     xp[f] = xq + (int64_t)m * K + 32 * lg;
     xs[f] = x_scale + m;
   }
-  v4f acc[NF][MF];
+  v4f acc[MF];
 #pragma unroll
-  for (int i = 0; i < NF; ++i)
-#pragma unroll
-    for (int f = 0; f < MF; ++f) acc[i][f] = v4f{0, 0, 0, 0};
+  for (int f = 0; f < MF; ++f) acc[f] = v4f{0, 0, 0, 0};
   const int whole = K / kScaleBlock;
   for (int j0 = wave; j0 < groups; j0 += kGemvWaves * AHEAD) {
-    v4i w[AHEAD][NF][2], x[AHEAD][MF][2];
+    v4i w[AHEAD][2], x[AHEAD][MF][2];
     float sx[AHEAD][MF], sw[AHEAD];
     const int live = j0 + (AHEAD - 1) * kGemvWaves < whole ? AHEAD : 0;      // all blocks whole: no checks
 #pragma unroll
@@ -459,13 +534,11 @@ __global__ __launch_bounds__(kThreads) void k_gemv_block(const uint8_t* __restri
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int j = j0 + u * kGemvWaves, jc = j < groups ? j : groups - 1;
-      sw[u] = ws[0][jc];
+      sw[u] = ws[jc];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = jc * kScaleBlock + 16 * h;
-        const bool in = live || (j < groups && k + 32 * lg < K);
-#pragma unroll
-        for (int i = 0; i < NF; ++i) w[u][i][h] = in ? *(const v4i*)(wp[i] + k) : v4i{0, 0, 0, 0};
+        w[u][h] = live || (j < groups && k + 32 * lg < K) ? *(const v4i*)(wp + k) : v4i{0, 0, 0, 0};
       }
     }
 #pragma unroll
@@ -473,17 +546,13 @@ __global__ __launch_bounds__(kThreads) void k_gemv_block(const uint8_t* __restri
 #pragma unroll
       for (int f = 0; f < MF; ++f) {
         const float sc = sw[u] * sx[u][f];
-        const v8i xv = join8(x[u][f][0], x[u][f][1]);
+        const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join8(w[u][0], w[u][1]), join8(x[u][f][0], x[u][f][1]),
+                                                                      v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < NF; ++i) {
-          const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join8(w[u][i][0], w[u][i][1]), xv, v4f{0, 0, 0, 0}, 0,
-                                                                        0, 0, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][f][r] = __builtin_fmaf(sc, p[r], acc[i][f][r]);
-        }
+        for (int r = 0; r < 4; ++r) acc[f][r] = __builtin_fmaf(sc, p[r], acc[f][r]);
       }
   }
-  gemv_store<MF, NF, YDT>(acc, part, wave, lane, M, N, n0, bias, y);
+  gemv_store<MF, YDT>(acc, part, wave, lane, M, N, n0, bias, y);
 }
 
 // Up to kFusedM tokens: the activations are quantized on the way, each wave
@@ -510,7 +579,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_block_fused(const void* __res
   const uint8_t* const wp = wq + (int64_t)n * K + 32 * lg;
   const float* const ws = w_scale + (int64_t)(n0 / kScaleBlock) * groups;
   const int mr = lr < M ? lr : M - 1;
-  v4f acc[1][1] = {{v4f{0, 0, 0, 0}}};
+  v4f acc[1] = {v4f{0, 0, 0, 0}};
   for (int j0 = wave; j0 < groups; j0 += kGemvWaves * AHEAD) {
     // this lane's 16 features, of block lane / 8
     const int kx = (j0 + (lane >> 3) * kGemvWaves) * kScaleBlock + 16 * (lane & 7);
@@ -570,39 +639,33 @@ __global__ __launch_bounds__(kThreads) void k_gemv_block_fused(const void* __res
       const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join8(w[u][0], w[u][1]), join8(c[0], c[1]),
                                                                      v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[0][0][r] = __builtin_fmaf(sc, p[r], acc[0][0][r]);
+      for (int r = 0; r < 4; ++r) acc[0][r] = __builtin_fmaf(sc, p[r], acc[0][r]);
     }
   }
-  gemv_store<1, 1, YDT>(acc, part, wave, lane, M, N, n0, bias, y);
+  gemv_store<1, YDT>(acc, part, wave, lane, M, N, n0, bias, y);
 }
 
 template <int YDT>
 hipError_t launch_product(const uint8_t* xq, const float* xs, int M, int K, const uint8_t* wq, const float* ws, int N,
                           const float* bias, void* y, hipStream_t st) {
-  if (M <= 64) {
-    // 32 weight rows a workgroup halve the activation reads (16 tokens, 14336 x 4096: 15.2 against
-    // 20.6 us) where that still gives every CU a workgroup
-    const bool wide = N >= 32 * 256;
-    const unsigned grid = (unsigned)((N + (wide ? 31 : 15)) / (wide ? 32 : 16));
-    if (M <= 16) {
-      if (wide) k_gemv_block<1, 2, 2, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-      else k_gemv_block<1, 1, 8, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-    } else if (M <= 32) {
-      if (wide) k_gemv_block<2, 2, 2, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-      else k_gemv_block<2, 1, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-    } else {
-      if (wide) k_gemv_block<4, 2, 2, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-      else k_gemv_block<4, 1, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-    }
-    return hipGetLastError();
+  auto tiles = [&](int64_t bm, int64_t bn) { return (unsigned)(((M + bm - 1) / bm) * ((N + bn - 1) / bn)); };
+  // Times are a product's alone, K = 4096.  Straight into registers where few tokens
+  // meet few weight rows (16 tokens: 6.2 against 9.7 us at 4096 rows, 10.1 against 10.2 at 8192 and
+  // 18.7 against 10.9 at 14336; 32 tokens: 8.4 against 9.9; 48: 11.6 against 10.1).
+  if (M <= 32 && N < 8192) {
+    const unsigned grid = (unsigned)((N + 15) / 16);
+    if (M <= 16) k_gemv_block<1, 8, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+    else k_gemv_block<2, 4, YDT><<<grid, kThreads, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+  } else if (tiles(64, 64) <= 512) {
+    // as long as the chip holds all of them, two a CU (4096 columns: 18.0 against 18.6 us for 512
+    // tokens, 24.6 against 18.5 for 576); 8 waves (4: 12.0 against 11.4 us at 512 x 2048)
+    k_gemm_tiles<64, 64, 2, 4, 4, YDT><<<tiles(64, 64), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+  } else if (tiles(256, 256) < 192) {
+    // 59.6 against 62.2 us at 2816 x 4096 (176 tiles of 256), 76.0 against 64.6 at 1024 x 14336 (224)
+    k_gemm_tiles<128, 128, 2, 4, 4, YDT><<<tiles(128, 128), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
+  } else {
+    k_gemm_tiles<256, 256, 2, 4, 2, YDT><<<tiles(256, 256), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
   }
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192)
-    k_gemm_tiles<256, 256, 2, 4, 2, YDT><<<(unsigned)tiles(256, 256), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-  else if (tiles(128, 128) >= 192)
-    k_gemm_tiles<128, 128, 2, 4, 4, YDT><<<(unsigned)tiles(128, 128), 512, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
-  else
-    k_gemm_tiles<64, 64, 2, 2, 4, YDT><<<(unsigned)tiles(64, 64), 256, 0, st>>>(xq, xs, M, K, wq, ws, N, bias, y);
   return hipGetLastError();
 }
 
