@@ -785,22 +785,38 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
   p.per = rows <= kSmallRows ? kSmallRows
           : dim == 256 || (dim == 64 && pairs * ((rows + 255) / 256) < 256) ? 128 : 256;
   p.blocks = (rows + p.per - 1) / p.per;
-  int64_t keys = max_kv;
-  if (window > 0 && window + max_q + 2 * kTile < keys) keys = window + max_q + 2 * kTile;
   const int64_t groups = pairs * p.blocks;
-  const int64_t step = 512;
-  // Splits to fill the chip, none where the sequences and heads do it alone (64 sequences, 8 kv heads,
-  // up to 4099 keys: 74 us whole, 77 + 5 in 1024-key shares).  Few rows: none longer than 8192 keys
-  // either, so that one long sequence among many does not hold up the rest; many rows are cut by
-  // rows, and a split would only add their partial sums' traffic.
-  int64_t want = p.per == kSmallRows ? (groups >= 512 ? 1 : 1024 / groups) : groups >= 192 ? 1 : 512 / groups;
-  if (p.per == kSmallRows && want < keys / 8192) want = keys / 8192;
-  const int64_t most = (keys + step - 1) / step;
-  want = want > most ? most : want;
+  // keys that a workgroup's rows see
+  const int64_t block_q = p.blocks > 1 ? p.per * max_q / rows + 2 : max_q;
+  int64_t keys = max_kv;
+  if (window > 0 && window + block_q + 2 * kTile < keys) keys = window + block_q + 2 * kTile;
+  int64_t want, least;      // splits, and keys of one
+  if (p.per == kSmallRows) {
+    // Splits to fill the chip, none where the sequences and heads do it alone (64 sequences, 8 kv heads,
+    // up to 4099 keys: 74 us whole, 77 + 5 in 1024-key shares), but none longer than 8192 keys either,
+    // so that one long sequence among many does not hold up the rest.  A share under 1024 keys costs
+    // the join more than it saves.
+    want = groups >= 512 ? 1 : 1024 / groups;
+    if (want < keys / 8192) want = keys / 8192;
+    least = 1024;
+  } else {
+    // As many as give every CU a workgroup, where the steps that they take off the longest one are worth
+    // the join: its launch and the partial sums that it writes and reads back (32-bit, at some 4.5 TB/s).
+    // One sequence, 32 heads, 8 kv heads, 128 features, 512 new tokens on 8192: 4 splits 102 us, 8 splits
+    // 113; 5 sequences, 8 heads of each, 28 on 920: 6 splits 18 us, none 34; 5 sequences, 4 heads of
+    // each, 576 on 61, window 256: 4 splits 36 us, none 31.
+    const double step_us = (double)(kStep * p.per * dim) / (64 * 256 * 128) * 1.8;
+    const double whole = (double)keys / kStep * step_us, unit = (double)(pairs * rows) * dim * 8 / 4.5e6;
+    want = 256 / groups;
+    const int64_t worth = (int64_t)__builtin_sqrt(whole / unit);
+    want = want > worth ? worth : want;
+    if (want > 1 && whole / want + 5.0 + unit * want > whole) want = 1;
+    least = 128;
+  }
   want = want > kMaxSplits ? kMaxSplits : want;
   want = want < 1 ? 1 : want;
-  int64_t c = ((keys + want - 1) / want + step - 1) / step * step;
-  c = c < 2 * step ? 2 * step : c;     // a shorter share costs the join more than it saves
+  int64_t c = ((keys + want - 1) / want + least / 2 - 1) / (least / 2) * (least / 2);
+  c = c < least ? least : c;
   p.splits = (int)((keys + c - 1) / c);
   if (p.splits < 1) p.splits = 1;
   p.chunk = (int)c;
