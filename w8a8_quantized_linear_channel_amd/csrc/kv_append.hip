@@ -164,8 +164,8 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     const bool active = have && patch < SH::kPatches;
     if (!active) i0 = i1 = 0;
     auto row = [&](int i) { return (int64_t)(first + (base + i - past)) * stride + (int64_t)head * D; };
-    // more than two new tokens in the patch: all its places at once (those without a new token repeat
-    // one that is, and are not stored); one or two, as in decoding: one after the other
+    // more than two new tokens in the patch: four at once (places without a new token repeat one that
+    // is, and are not stored); one or two, as in decoding: one after the other
     const bool many = i1 - i0 > 2;
     float amax = 0.0f;
     // Read once for the maximum and once more (from the caches) for the codes: kept in registers instead,
@@ -180,7 +180,7 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     };
     if (many) {
 #pragma unroll 1
-      for (int i = 0; i < kPatch; i += 4) {
+      for (int i = i0; i < i1; i += 4) {
         float v[4][8];
         four(i, v);
 #pragma unroll
@@ -246,14 +246,14 @@ __device__ void append_pages(const AppendArgs& a, int s, int j0, int group, floa
     if (many) {
       if (!is_v) {
 #pragma unroll 1
-        for (int i = 0; i < kPatch; i += 4) {
+        for (int i = i0; i < i1; i += 4) {
           float v[4][8];
           four(i, v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t q0, q1;
             codes(v[j], q0, q1);
-            if (i + j >= i0 && i + j < i1) *(v2i*)(kc + (i + j) * D) = v2i{(int)q0, (int)q1};
+            if (i + j < i1) *(v2i*)(kc + (i + j) * D) = v2i{(int)q0, (int)q1};
           }
         }
       } else {
