@@ -238,6 +238,16 @@ def test_attention_heads(Hq, Hk, causal):
     run_attention(rng, [1, 2, 3], [300, 77, 3], Hq, Hk, 64, 32, BF, causal=causal, strided=True)
 
 
+@pytest.mark.parametrize("D,page,dt", [(64, 32, HF), (128, 64, BF), (256, 128, HF)])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,length", [([9, 1, 0, 5], [900, 1, 70, 1500]), ([30, 7, 29], [30, 2000, 333])])
+def test_attention_few_rows(D, page, dt, window, causal, new, length):
+    """Several blocks of 16 rows a sequence, a last one that is not full, sequences with fewer."""
+    rng = np.random.default_rng(D + window + len(new))
+    run_attention(rng, new, length, 6, 2, D, page, dt, causal=causal, window=window)
+
+
 @pytest.mark.parametrize("D,page,dt", [(64, 32, HF), (128, 64, BF), (128, 128, HF), (256, 64, BF), (256, 32, HF),
                                        (64, 128, BF), (128, 32, BF)])
 @pytest.mark.parametrize("window", [0, 50])

@@ -1,9 +1,9 @@
 // Attention of new queries over the paged 8-bit key/value cache.
 //
-// Up to 16 rows (query tokens x the query heads that share a kv head): one
-// workgroup takes them with one sequence, kv head and share of the keys; its NW
-// waves take 64-key tiles in turn and join at the end.  Each wave computes
-// S^T = K Q^T with v_mfma_f32_16x16x32 (16 keys x 16 rows), so lane (q, g)
+// Few rows (query tokens x the query heads that share a kv head): a workgroup
+// takes 16 with one sequence, kv head and share of the keys; its NW waves take
+// 64-key tiles in turn and join at the end.  Each wave computes S^T = K Q^T
+// with v_mfma_f32_16x16x32 (16 keys x 16 rows), so lane (q, g)
 // (q = lane % 16, g = lane / 16) holds scores of row q.  The keys of the four
 // 16-key MFMA tiles are dealt so that lane group g ends up with the 16
 // consecutive keys 16 g .. 16 g + 15: tile t's row 4 g + i is key 16 g + 4 t + i.
@@ -778,7 +778,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks,
   }
 }
 
-constexpr int kSmallRows = 16;      // up to here one 16-row tile
+constexpr int kSmallRows = 16;      // of a workgroup where there are few rows
 
 // How a call is cut: rows of one workgroup, row blocks of a sequence, splits of the keys and keys of
 // one split.
@@ -789,10 +789,21 @@ struct Plan {
 Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
   Plan p;
   const int64_t pairs = (int64_t)seqs * kv_heads;
+  int64_t seen = max_kv;
+  if (window > 0 && window + max_q < seen) seen = window + max_q;
+  // Few rows, 16 a workgroup: up to 64, and up to 128 where the blocks of 16 together read no more than
+  // half a million keys (8 kv heads of 128 features, this way against many rows': 24 rows on 300 keys
+  // 7.7 against 13.7 us, 64 on 110000 127 against 131, 32 sequences of 64 on 2000 64 against 77, 8 of 128
+  // on 300 12 against 21, one of 128 on 16000 42 against 34).  256 features, one wave a SIMD and half the
+  // bytes in flight: beyond 16 rows only up to a quarter of a million (2 sequences of 128 on 2000 30
+  // against 38, of 64 on 10000 76 against 49).
+  const int64_t keys_read = pairs * ((rows + kSmallRows - 1) / kSmallRows) * seen;
+  const bool few = rows <= kSmallRows || (dim < 256 && rows <= 64) ||
+                   (rows <= 128 && keys_read <= (int64_t)1 << (dim < 256 ? 19 : 18));
   // Many rows: 8 waves (two on a SIMD) share a step's codes; 4 at 256 features, whose accumulators,
   // queries and scores fit a wave only where it has the SIMD's registers to itself, and at 64 features
   // where blocks of 256 rows would leave CUs without one.
-  p.per = rows <= kSmallRows ? kSmallRows
+  p.per = few ? kSmallRows
           : dim == 256 || (dim == 64 && pairs * ((rows + 255) / 256) < 256) ? 128 : 256;
   p.blocks = (rows + p.per - 1) / p.per;
   const int64_t groups = pairs * p.blocks;
@@ -830,6 +841,7 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
   p.splits = (int)((keys + c - 1) / c);
   if (p.splits < 1) p.splits = 1;
   p.chunk = (int)c;
+  if (few && p.blocks > 65535 / seqs) p.blocks = 65535 / seqs;
   const int64_t most_blocks = ((int64_t)1 << 30) / (pairs * p.splits);
   if (p.blocks > most_blocks) p.blocks = most_blocks;
   if (p.blocks < 1) p.blocks = 1;
