@@ -797,9 +797,9 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
   // on 300 12 against 21, one of 128 on 16000 42 against 34).  256 features, one wave a SIMD and half the
   // bytes in flight: beyond 16 rows only up to a quarter of a million (2 sequences of 128 on 2000 30
   // against 38, of 64 on 10000 76 against 49).
-  const int64_t keys_read = pairs * ((rows + kSmallRows - 1) / kSmallRows) * seen;
   const bool few = rows <= kSmallRows || (dim < 256 && rows <= 64) ||
-                   (rows <= 128 && keys_read <= (int64_t)1 << (dim < 256 ? 19 : 18));
+                   (rows <= 128 && pairs * ((rows + kSmallRows - 1) / kSmallRows) * seen <=
+                                       (int64_t)1 << (dim < 256 ? 19 : 18));
   // Many rows: 8 waves (two on a SIMD) share a step's codes; 4 at 256 features, whose accumulators,
   // queries and scores fit a wave only where it has the SIMD's registers to itself, and at 64 features
   // where blocks of 256 rows would leave CUs without one.
@@ -827,7 +827,7 @@ Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64
     // 113; 5 sequences, 8 heads of each, 28 on 920: 6 splits 18 us, none 34; 5 sequences, 4 heads of
     // each, 576 on 61, window 256: 4 splits 36 us, none 31.
     const double step_us = (double)(kStep * p.per * dim) / (64 * 256 * 128) * 1.8;
-    const double whole = (double)keys / kStep * step_us, unit = (double)(pairs * rows) * dim * 8 / 4.5e6;
+    const double whole = (double)keys / kStep * step_us, unit = (double)pairs * (double)rows * dim * 8 / 4.5e6;
     want = 256 / groups;
     const int64_t worth = (int64_t)__builtin_sqrt(whole / unit);
     want = want > worth ? worth : want;
