@@ -416,9 +416,11 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
  *     w_j = softmax_j(scale q . k_j),   out = sum_j w_j v_j,   lse = log sum_j exp(scale q . k_j)
  * A query that sees no key gets out = 0 and lse = -inf.  Codes of keys that no
  * query sees may hold anything, NaN codes included, and pages that lie wholly
- * there need not exist.  Scores and values are exact products of the codes with
- * the 16-bit queries and with the softmax weights rounded to f16; all sums,
- * the maximum and the output accumulator are binary32.
+ * there need not exist.  Scores are exact products of codes and 16-bit queries.
+ * The weight of a key's value codes, w_j times its page's 2^(b - 127), is
+ * rounded to f16 (2^-11 of it, or 2^-24 of the row's largest such weight where
+ * that is more); its products with the codes are exact.  All sums, the maximum
+ * and the output accumulator are binary32.
  * q: [T, Hq, D] of `dtype` (F16 or BF16), tokens q_stride elements apart (a
  * multiple of 8); out: [T, Hq, D] of dtype; lse: float [T, Hq] or NULL.  Rows of
  * tokens that belong to no sequence are left alone.  Hq is a multiple of Hkv.

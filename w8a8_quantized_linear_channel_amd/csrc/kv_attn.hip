@@ -18,11 +18,18 @@
 // us, a chain of page table, exponents, codes and the waves' join.
 //
 // e4m3 codes convert to bf16 / f16 exactly (4 significant bits).  The key
-// exponent of a page multiplies the scores (one factor per lane and tile: 32
-// keys lie in one page).  Values enter the product relative to the largest
-// exponent byte seen so far (f16 holds 2^-24 .. 65504), which the accumulator
-// is rescaled to; the softmax weights are rounded to f16 (2^-12 of a weight),
-// and maximum, sum and accumulator are held in 32 bits.
+// exponent of a page multiplies the scores, the value exponent the softmax
+// weights (one factor of each per lane and tile: 32 keys lie in one page), so
+// value codes enter the product as they are.  What is rounded to f16 (2^-11 of
+// it) is p_j 2^(b_j - e), p_j = 2^(s_j - m): the weight of a key's codes, e a
+// whole number that each row holds beside its maximum m.  While every page that
+// a row sees has |b_j - e| <= gap, e stays and the exponent is part of the
+// exponential's argument; elsewhere e is moved so that the largest weight so far
+// is about 1 (a wave's slow step, with the softmax sum taken from exponentials
+// of its own).  Either way the row's largest weight is at least 2^-1 and none
+// passes 2^15, so what f16 cannot hold is below 2^-24 of the row's largest, and
+// pages that the row's mask hides do not enter at all.  Maximum, sum and
+// accumulator are held in 32 bits.
 #include <type_traits>
 #include <utility>
 
@@ -59,8 +66,15 @@ __device__ __forceinline__ v4i widen8(int lo, int hi, float scale) {
                __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true))};
 }
 
+__device__ __forceinline__ v4f scaled4(const v4f v, int e) {
+  return v4f{__builtin_ldexpf(v[0], e), __builtin_ldexpf(v[1], e), __builtin_ldexpf(v[2], e), __builtin_ldexpf(v[3], e)};
+}
+
 // 2^(b - 127) as a float for an exponent byte b in [0, 254]
 __device__ __forceinline__ float exp_byte(int b) { return __uint_as_float(b > 0 ? (uint32_t)b << 23 : 0x400000u); }
+
+// The whole number e of a row that has seen no key (any page is out of its gap)
+constexpr float kNoExp = -65536.0f;
 
 // The rows of one sequence and the keys any of them sees.
 struct Span {
@@ -90,6 +104,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
   constexpr int KS = D / 32;        // MFMA steps over the features
   constexpr int KL = D / 64;        // 16-byte loads of a lane's share of a key
   constexpr int NT = D / 16;        // 16-feature tiles of the output
+  // weights p 2^(b - e + kUp), p <= 1: the largest from 2^(kUp - kGap) to 2^15
+  constexpr float kGap = 7.0f, kUp = 8.0f;
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -133,8 +149,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
     const int kb1 = split + 1 < (int)gridDim.x && kb0 + (int64_t)chunk < khi ? kb0 + chunk : khi;
 
     v4f acc[NT];
-    float m = -INFINITY, l = 0.0f;
-    int bmax = 0;          // the values' reference exponent byte
+    float m = -INFINITY, l = 0.0f, e = kNoExp;
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
 
@@ -201,41 +216,48 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
           sc[t][i] = x;
           mx = fmaxf(mx, x);
         }
-      // over the row's four lanes: the maximum, and the values' largest exponent
-      const bool seen = keyv < khi && keyv + 16 > klo;
-      int bt = seen ? vb : 0;
+      // over the row's four lanes; a lane without a visible key has no say about the exponents
+      const bool seen = mx > -INFINITY;
+      const float own = mx + (float)vb;
+      float gap = seen ? (float)vb - e : 0.0f;
       mx = fmaxf(mx, __shfl_xor(mx, 16));
-      bt = max(bt, __shfl_xor(bt, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      bt = max(bt, __shfl_xor(bt, 32));
-      const int bnew = bt > bmax ? bt : bmax;
-      const int drop = bmax - bnew;
-      const float vfix = __builtin_ldexpf(1.0f, drop < -126 ? -126 : drop);
-      bmax = bnew;
-      int down = seen ? vb - bmax : 0;
-      down = down < -126 ? -126 : down;
-      const float vscale = __builtin_ldexpf(1.0f, down);
-
       const float mn = fmaxf(m, mx);
       const float ref = mn == -INFINITY ? 0.0f : mn;
       const float alpha = __builtin_amdgcn_exp2f(m - ref);
+      float fix = alpha, share = __builtin_amdgcn_exp2f(-(gap + kUp));
+      l *= alpha;
+      if (__any(fabsf(gap) > kGap)) {
+        // the largest weight so far, 2^top (that of the keys before to within the gap)
+        float top = fmaxf(own, __shfl_xor(own, 16));
+        top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m + e);
+        const float to = mn == -INFINITY ? e : ceilf(top - mn);
+        fix = __builtin_amdgcn_exp2f(m - ref + (e - to));
+        e = to;
+        gap = seen ? (float)vb - e : 0.0f;
+        share = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l += __builtin_amdgcn_exp2f(sc[t][i] - ref);
+      }
       m = mn;
+      const float wref = ref - (gap + kUp);
       float sum = 0.0f;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sc[t][i] = __builtin_amdgcn_exp2f(sc[t][i] - ref);
+          sc[t][i] = __builtin_amdgcn_exp2f(sc[t][i] - wref);
           sum += sc[t][i];
         }
-      l = l * alpha + sum;
+      l = __builtin_fmaf(sum, share, l);
       v4i pf[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         pf[j] = v4i{(int)pack2_out<DT_F16>(sc[2 * j][0], sc[2 * j][1]), (int)pack2_out<DT_F16>(sc[2 * j][2], sc[2 * j][3]),
                     (int)pack2_out<DT_F16>(sc[2 * j + 1][0], sc[2 * j + 1][1]),
                     (int)pack2_out<DT_F16>(sc[2 * j + 1][2], sc[2 * j + 1][3])};
-      const float fix = alpha * vfix;
       if (__any(fix != 1.0f)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n] *= fix;
@@ -256,8 +278,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][0], vx[n][1], vscale), pf[0], acc[n]);
-        acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][2], vx[n][3], vscale), pf[1], acc[n]);
+        acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][0], vx[n][1], 1.0f), pf[0], acc[n]);
+        acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][2], vx[n][3], 1.0f), pf[1], acc[n]);
       }
     };
     Tile one, two;
@@ -279,10 +301,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
     // join the waves
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    const float vtrue = exp_byte(bmax);
+    const int unit = (int)(e - (127.0f + kUp));
     __syncthreads();                 // the row tile before is read
 #pragma unroll
-    for (int n = 0; n < NT; ++n) *(v4f*)&s_acc[wave][lr][16 * n + 4 * lg] = acc[n] * vtrue;
+    for (int n = 0; n < NT; ++n) *(v4f*)&s_acc[wave][lr][16 * n + 4 * lg] = scaled4(acc[n], unit);
     if (lg == 0) {
       s_ml[wave][lr][0] = m;
       s_ml[wave][lr][1] = l;
@@ -345,8 +367,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
 // weights are the B operand of O^T = V^T P^T as they stand.
 //
 // The running maximum is a reference that is only moved when a score passes it
-// by 2^8 (weights up to 256 fit f16 and cost no precision): most steps neither
-// rescale nor exchange anything between lanes.
+// by 8 (p up to 2^8 costs no precision): most steps neither rescale nor exchange
+// anything between lanes.
 //
 // Bound by the matrix units at the clock that the power leaves them: the prompt
 // of 8192 tokens is 550 G flop in 580 us, 0.95 PFLOP/s (a plain 8192^3 product
@@ -392,11 +414,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
   constexpr int kChunks = kStep * D / 16;        // 16-byte chunks of codes of a step's keys, and of its values
   constexpr int kPer = 2 * kChunks / kThr;       // of a thread
   static_assert(kPer >= 1 && 2 * kChunks % kThr == 0 && kChunks % 64 == 0, "load split");
+  // weights p 2^(b - e + kUp), p <= 2^8: the largest from 2^(kUp - kGap) to 2^15
+  constexpr float kGap = 4.0f, kUp = 3.0f;
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * 2 * kTileBytes];
   // byte offset of the page's head, and the exponent bytes (keys | values << 8), of each 32-key half
   // of up to kMeta / 2 steps
   __shared__ int64_t s_page[kMeta];
-  __shared__ int s_exp[kMeta], s_top[NW];
+  __shared__ int s_exp[kMeta];
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -450,8 +474,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     v16 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = v16{};
-    float m = -INFINITY, l = 0.0f;
-    int bmax = 0;                                // the values' reference exponent byte
+    float m = -INFINITY, l = 0.0f, e = kNoExp;
 
     // chunk j of this thread: codes tid + j threads, the keys' (of step ik) first, then the values' (of iv)
     v4i code[kPer];
@@ -511,16 +534,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         __builtin_amdgcn_sched_barrier(0);
         *(v4i*)(at + (place ^ 16)) = widen8<DT>(pick(swap, x2, x0), pick(swap, x3, x1), 1.0f);
       } else {
-        int down = (s_exp[(2 * iv + ((tid & 3) >> 1)) & (kMeta - 1)] >> 8) - bmax;
-        down = down < -126 ? -126 : down;
-        const float vscale = __uint_as_float((uint32_t)(127 + down) << 23);
         const int row = (c - kChunks) / 4, src = c & 3;
         const int odd = row & 1, swap = -odd;
         uint8_t* const at = smem + (2 + (iv & 1)) * kTileBytes + row * 128;
         const int place = ((2 * src + odd) ^ val_swz(row)) << 4;
-        *(v4i*)(at + place) = widen8<DT_F16>(pick(swap, x0, x2), pick(swap, x1, x3), vscale);
+        *(v4i*)(at + place) = widen8<DT_F16>(pick(swap, x0, x2), pick(swap, x1, x3), 1.0f);
         __builtin_amdgcn_sched_barrier(0);
-        *(v4i*)(at + (place ^ 16)) = widen8<DT_F16>(pick(swap, x2, x0), pick(swap, x3, x1), vscale);
+        *(v4i*)(at + (place ^ 16)) = widen8<DT_F16>(pick(swap, x2, x0), pick(swap, x3, x1), 1.0f);
       }
     };
     auto put = [&](int ik, int iv) {
@@ -540,7 +560,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     };
     v16 sc[2], sn[2];
     v4i pf[4];
-    float kscale = 0.0f;
+    float kscale = 0.0f, wref = 0.0f, share = 0.0f;
     auto scores = [&](int i) {
       sn[0] = v16{};
       sn[1] = v16{};
@@ -558,8 +578,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sn[t][r]);
       return mx;
     };
-    // the scores of step i (largest: mx) become the current ones
-    auto settle = [&](int i, int kb, float mx) {
+    // the scores of the step at kb (exponents exps, largest mx) become the current ones; `again`: they
+    // have been before (the last step's, once more at its end)
+    auto settle = [&](int exps, int kb, float mx, bool again) {
       if (!(kb >= all_lo && kb + kStep <= all_hi)) {
         // register 16 t + r is key kb + 32 h + 16 t + r: the row sees those from `low` to below `high`
         const int high = (a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total) - kb - 32 * lh;
@@ -571,17 +592,41 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         mx = highest();
       }
       // not 0: a masked score of -inf stays one
-      kscale = fmaxf(exp_byte(s_exp[2 * i + lh] & 255) * scale, 1.17549435e-38f);
+      kscale = fmaxf(exp_byte(exps & 255) * scale, 1.17549435e-38f);
       mx *= kscale;
-      if (__any(mx > m + 8.0f)) {
+      // a lane without a visible key has no say about the exponents
+      const bool seen = mx > -INFINITY;
+      const float vb = (float)(exps >> 8), own = mx + vb;
+      float gap = seen ? vb - e : 0.0f;
+      share = __builtin_amdgcn_exp2f(-(gap + kUp));
+      if (__any(mx > m + 8.0f || fabsf(gap) > kGap)) {
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m, mx);
-        const float alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
-        m = mn;
-        l *= alpha;
+        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.0f : mn;
+        float fix = __builtin_amdgcn_exp2f(m - ref);
+        l *= fix;
+        if (__any(fabsf(gap) > kGap)) {
+          // the largest weight so far, 2^top (that of the keys before to within the gap)
+          const float top = fmaxf(fmaxf(own, __shfl_xor(own, 32)), m + e);
+          const float to = mn == -INFINITY ? e : ceilf(top - mn);
+          fix = __builtin_amdgcn_exp2f(m - ref + (e - to));
+          e = to;
+          gap = seen ? vb - e : 0.0f;
+          share = 0.0f;
+          if (!again) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] *= alpha;
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                l += __builtin_amdgcn_exp2f(__builtin_fmaf(sn[t][r], kscale, -ref));
+                asm volatile("" : "+v"(l));        // one after the other: the registers are all taken
+              }
+          }
+        }
+        m = mn;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] *= fix;
       }
+      wref = (m == -INFINITY ? 0.0f : m) - (gap + kUp);
       sc[0] = sn[0];
       sc[1] = sn[1];
     };
@@ -597,31 +642,17 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
       const int n = steps - run < kMeta / 2 ? steps - run : kMeta / 2;
       const int kb_run = kb0 + run * kStep;
       __syncthreads();                           // the run before is read
-      int top = 0;
       if (tid < kMeta) {
-        // a half that no row sees reads page 0 and counts as values of exponent 0
+        // a half that no row sees reads page 0
         const int key = kb_run + 32 * tid;
         const bool seen = key < khi && key + 32 > klo;
         int p = seen ? kv.table[(int64_t)s * kv.max_pages + key / kv.page] : 0;
         p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
         p = p * kv.kv_heads + head;
         s_page[tid] = (int64_t)p * (kv.page * D);
-        top = seen && tid < 2 * n ? kv.ve[p] : 0;
-        s_exp[tid] = kv.ke[p] | top << 8;
+        s_exp[tid] = kv.ke[p] | kv.ve[p] << 8;
       }
-      // values enter the product relative to the largest exponent so far
-      const float wtop = wave_max((float)top);
-      if (lane == 0) s_top[wave] = (int)wtop;
       __syncthreads();
-      int bn = bmax;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) bn = s_top[w] > bn ? s_top[w] : bn;
-      if (bn > bmax && run > 0) {
-        const float fix = __builtin_ldexpf(1.0f, bmax - bn < -126 ? -126 : bmax - bn);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] *= fix;
-      }
-      bmax = bn;
       // Step i multiplies the next step's scores beside its own softmax and puts the codes of the steps
       // after into the buffers that step i - 1 has left.
       load(0, 0, n, kb_run);
@@ -631,7 +662,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
       put(1, 0);
       meet();
       scores(0);
-      settle(0, kb_run, highest());
+      settle(s_exp[lh], kb_run, highest(), false);
       load(2, 1, n, kb_run);
       meet();
       for (int i = 0; i < n; ++i) {
@@ -644,7 +675,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         constexpr int kAheadOps = 4, kKeyOps = 2 * KS, kValOps = 4 * NT;
         constexpr int kShare = 32 / kKeyOps, kSeek = 32 / kValOps;
         static_assert(kKeyOps % kAheadOps == 0, "the ring of operands runs on from the keys' to the values'");
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const int exps = s_exp[2 * next + lh];
         v4i op[kAheadOps];
 #pragma unroll
         for (int x = 0; x < kAheadOps; ++x) op[x] = key_op(i + 1, x);
@@ -659,7 +690,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
 #pragma unroll
           for (int e = x * kShare; e < (x + 1) * kShare; ++e) {
             const int t = e >> 4, r = e & 15;
-            sc[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], kscale, -ref));
+            sc[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], kscale, -wref));
             sum += sc[t][r];
             if ((e & 7) == 7)
               pf[e >> 3] = v4i{(int)pack2_out<DT_F16>(sc[t][r - 7], sc[t][r - 6]), (int)pack2_out<DT_F16>(sc[t][r - 5], sc[t][r - 4]),
@@ -668,7 +699,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
           asm volatile("" : "+v"(sum));
           __builtin_amdgcn_sched_barrier(0);
         });
-        l += sum;
+        l = __builtin_fmaf(sum, share, l);
         each<kValOps>([&](auto X) {
           constexpr int x = decltype(X)::value;
           acc[x % NT] = mma32<DT_F16>(op[x % kAheadOps], pf[x / NT], acc[x % NT]);
@@ -687,7 +718,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
             }
           });
         });
-        settle(next, kb_run + next * kStep, mx);
+        settle(exps, kb_run + next * kStep, mx, i + 1 == n);
         meet();
       }
     }
@@ -698,16 +729,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     asm volatile("" : "+v"(again));
     const int orw = r0 + 32 * wave + again;
     if (orw < rows) {
-      const float vtrue = exp_byte(bmax);
+      const int unit = (int)(e - (127.0f + kUp));
       const int otok = orw / group;
       const int64_t orow = (int64_t)(sp.first + otok) * a.heads + head * group + (orw - otok * group);
-      const float inv = (splits > 1 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f)) * vtrue;
+      const float inv = splits > 1 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 16; r += 4) {
           const int d = 32 * n + 2 * r + 4 * lh;
-          const v4f o = {acc[n][r] * inv, acc[n][r + 1] * inv, acc[n][r + 2] * inv, acc[n][r + 3] * inv};
+          const v4f o = scaled4(v4f{acc[n][r], acc[n][r + 1], acc[n][r + 2], acc[n][r + 3]} * inv, unit);
           if (splits > 1) *(v4f*)(a.part + ((int64_t)split * kv.tokens * a.heads + orow) * D + d) = o;
           else *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
         }
