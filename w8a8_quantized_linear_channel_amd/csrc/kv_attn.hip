@@ -76,6 +76,41 @@ __device__ __forceinline__ float exp_byte(int b) { return __uint_as_float(b > 0 
 // The whole number e of a row that has seen no key (any page is out of its gap)
 constexpr float kNoExp = -65536.0f;
 
+// NaN codes among the values.  A key that some rows of a block see and others do not enters the latter's
+// product with weight 0, which a NaN code turns into NaN.  A block whose sums hold a NaN goes through its
+// keys once more with such codes cleared, and puts the NaN where rows do see them afterwards; a block
+// without one pays for a sum.
+//
+// A word of codes without its NaN codes under mask (bit 7 of each byte that counts).
+__device__ __forceinline__ int without_nan(int x, uint32_t mask) {
+  const uint32_t t = (((uint32_t)x & 0x7f7f7f7fu) + 0x01010101u) & mask;
+  return x & (int)~((t << 1) - (t >> 7));
+}
+// NaN into the output of row `row` at position pos (of this split, share [kb0, kb1) of its keys) for the
+// features d0 + step i + 0 .. 3 in which a key that it sees, outside [all_lo, all_hi), holds a NaN code.
+template <int D>
+__device__ __forceinline__ void put_nan(const AttnArgs& a, int s, int head, int64_t row, int pos, int split, bool split_out,
+                                        int kb0, int kb1, int all_lo, int all_hi, int d0, int step) {
+  const KvView kv = a.kv;
+  int low = a.window > 0 ? pos - a.window + 1 : 0, high = a.causal && pos + 1 < kb1 ? pos + 1 : kb1;
+  low = low > kb0 ? low : kb0;
+  for (int key = low; key < high; ++key) {
+    if (key >= all_lo && key < all_hi) {
+      key = all_hi - 1;
+      continue;
+    }
+    int p = kv.table[(int64_t)s * kv.max_pages + key / kv.page];
+    p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
+    const uint8_t* const v = kv.v + ((int64_t)p * kv.kv_heads + head) * D * kv.page + (key & (kv.page - 1));
+#pragma unroll 1
+    for (int d = d0; d < D; d += (d & 3) == 3 ? step - 3 : 1) {
+      if ((v[d * kv.page] & 0x7f) != 0x7f) continue;
+      if (split_out) a.part[((int64_t)split * kv.tokens * a.heads + row) * D + d] = __builtin_nanf("");
+      else ((uint16_t*)a.out)[row * D + d] = 0x7fff;
+    }
+  }
+}
+
 // The rows of one sequence and the keys any of them sees.
 struct Span {
   int first, n;        // tokens [first, first + n) of the batch
@@ -120,8 +155,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
 
   __shared__ __attribute__((aligned(16))) float s_acc[NW][16][D + 4];
   __shared__ float s_ml[NW][16][2];
+  __shared__ int s_nan[NW];
 
-  for (int r0 = tile0 * 16; r0 < rows; r0 += row_tiles * 16) {
+  bool careful = false;              // the row tile is taken again, without NaN codes
+  for (int r0 = tile0 * 16; r0 < rows;) {
     // this lane's row and the keys that it sees: [low, high)
     const int row = r0 + lr, rc = row < rows ? row : rows - 1;
     const int tok = rc / group, hq = rc - tok * group;
@@ -142,6 +179,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
     const int pos0 = sp.past + r0 / group, pos1 = sp.past + last / group;
     const int klo = a.window > 0 && pos0 - a.window + 1 > 0 ? pos0 - a.window + 1 : 0;
     const int khi = a.causal ? (pos1 + 1 < sp.total ? pos1 + 1 : sp.total) : sp.total;
+    // those that all of them see, and whether there are others
+    const int all_lo = a.window > 0 && pos1 - a.window + 1 > 0 ? pos1 - a.window + 1 : 0;
+    const int all_hi = a.causal ? (pos0 + 1 < sp.total ? pos0 + 1 : sp.total) : sp.total;
+    const bool mixed = all_lo != klo || all_hi != khi;
     // this workgroup's share: `chunk` keys from a multiple of kTile on, the last share all that is left
     const int base = klo & ~(kTile - 1);
     const int64_t from = (int64_t)split * chunk;
@@ -276,6 +317,24 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
           for (int n = 0; n < NT; ++n) vx[n][w] &= (int)keep;
         }
       }
+      if (__builtin_expect(careful, 0)) {
+        int at = keyv;
+        asm volatile("" : "+v"(at));               // nothing of this ahead of the loop
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t some = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = at + 4 * w + i;
+            some |= key < all_lo || key >= all_hi ? 0x80u << (8 * i) : 0u;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            vx[n][w] = without_nan(vx[n][w], some);
+            __builtin_amdgcn_sched_barrier(0);       // one after the other: the registers are all taken
+          }
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         acc[n] = mma16<DT_F16>(widen8<DT_F16>(vx[n][0], vx[n][1], 1.0f), pf[0], acc[n]);
@@ -309,11 +368,27 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
       s_ml[wave][lr][0] = m;
       s_ml[wave][lr][1] = l;
     }
+    if (mixed) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sum += (acc[n][0] + acc[n][1]) + (acc[n][2] + acc[n][3]);
+      const int nan = __any(sum != sum);
+      if (lane == 0) s_nan[wave] = nan;
+    }
     __syncthreads();
+    if (mixed && !careful) {
+      int nan = s_nan[0];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) nan |= s_nan[w];
+      careful = nan != 0;
+      if (careful) continue;
+    }
     // 16 threads per row, each D / 16 features
-    const int row16 = tid >> 4, part = tid & 15;
+    int again = tid;               // (what it is split into need not live through the loop)
+    asm volatile("" : "+v"(again));
+    const int row16 = again >> 4, part = again & 15;
     const int orw = r0 + row16;
-    if (tid < 256 && orw < rows) {
+    if (again < 256 && orw < rows) {
       float mm = s_ml[0][row16][0];
 #pragma unroll
       for (int w = 1; w < NW; ++w) mm = fmaxf(mm, s_ml[w][row16][0]);
@@ -340,6 +415,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
           *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
         }
       }
+      if (__builtin_expect(careful, 0)) put_nan<D>(a, s, head, orow, sp.past + otok, split, split_out, kb0, kb1, all_lo, all_hi, part * 4, 64);
       if (part == 0) {
         if (split_out) {
           float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
@@ -350,6 +426,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
         }
       }
     }
+    careful = false;
+    r0 += row_tiles * 16;
   }
 }
 
@@ -421,6 +499,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
   // of up to kMeta / 2 steps
   __shared__ int64_t s_page[kMeta];
   __shared__ int s_exp[kMeta];
+  __shared__ int s_nan[NW];
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -437,8 +516,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
   const Span sp = span_of(a, s);
   const int rows = sp.n * group;
   const int tiles = (rows + kRows - 1) / kRows;
+  const int page_log2 = 31 - __builtin_clz(kv.page);
 
-  for (int tile = tiles - 1 - tile0; tile >= 0; tile -= row_tiles) {
+  bool careful = false;                          // the tile is taken again, without NaN codes
+  for (int tile = tiles - 1 - tile0; tile >= 0;) {
     const int r0 = tile * kRows;
     // this lane's row (rows past the end repeat the last one and are not stored)
     const int row = r0 + 32 * wave + lr, rc = row < rows ? row : rows - 1;
@@ -446,8 +527,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     const int pos = sp.past + tok;
     v4i qf[KS];
     {
+      int qh = lh;
+      asm volatile("" : "+v"(qh));               // (nor need this)
       const uint16_t* q = (const uint16_t*)a.q + (int64_t)(sp.first + tok) * a.q_stride +
-                          (int64_t)(head * group + hq) * D + lh * (D / 2);
+                          (int64_t)(head * group + hq) * D + qh * (D / 2);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         qf[ks] = *(const v4i*)(q + 8 * ks);
@@ -465,6 +548,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     const int pw0 = sp.past + w0 / group, pw1 = sp.past + w1 / group;
     const int all_hi = a.causal ? (pw0 + 1 < sp.total ? pw0 + 1 : sp.total) : sp.total;
     const int all_lo = a.window > 0 ? pw1 - a.window + 1 : 0;
+    // those that every row of the block does, and whether there are others
+    const int block_hi = a.causal ? (p0 + 1 < sp.total ? p0 + 1 : sp.total) : sp.total;
+    const int block_lo = a.window > 0 && p1 - a.window + 1 > 0 ? p1 - a.window + 1 : 0;
+    const bool mixed = block_lo != klo || block_hi != khi;
     const int base = klo & ~(kStep - 1);
     const int64_t from = (int64_t)split * chunk;
     const int kb0 = base + from < khi ? base + (int)from : khi;
@@ -502,6 +589,24 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     // are masked)
     auto clear = [&](int iv, int kb_run) {
       const int kb = kb_run + iv * kStep;
+      if (__builtin_expect(careful, 0)) {
+        int first = kb + 16 * (tid & 3);
+        asm volatile("" : "+v"(first));          // nothing of this ahead of the loop
+        each<kPer>([&](auto J) {
+          constexpr int j = decltype(J)::value;
+          if (is_key(j)) return;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t some = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = first + 4 * w + e;
+              some |= key < block_lo || key >= block_hi ? 0x80u << (8 * e) : 0u;
+            }
+            code[j][w] = without_nan(code[j][w], some);
+          }
+        });
+      }
       if (kb >= klo && kb + kStep <= khi) return;
       const int first = kb + 16 * (tid & 3);
       each<kPer>([&](auto J) {
@@ -646,7 +751,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         // a half that no row sees reads page 0
         const int key = kb_run + 32 * tid;
         const bool seen = key < khi && key + 32 > klo;
-        int p = seen ? kv.table[(int64_t)s * kv.max_pages + key / kv.page] : 0;
+        int p = seen ? kv.table[(int64_t)s * kv.max_pages + (key >> page_log2)] : 0;
         p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
         p = p * kv.kv_heads + head;
         s_page[tid] = (int64_t)p * (kv.page * D);
@@ -722,12 +827,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         meet();
       }
     }
+    if (mixed && !careful) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += acc[n][r];
+      const int found = __any(sum != sum);
+      __syncthreads();                           // the tile before has read its own
+      if (lane == 0) s_nan[wave] = found;
+      __syncthreads();
+      int nan = s_nan[0];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) nan |= s_nan[w];
+      careful = nan != 0;
+      if (careful) continue;
+    }
 
     l += __shfl_xor(l, 32);
     // the lane's row again (its place in the output need not live through the loop)
-    int again = lane & 31;
+    int again = __lane_id();
     asm volatile("" : "+v"(again));
-    const int orw = r0 + 32 * wave + again;
+    const int oh = again >> 5, orw = r0 + 32 * wave + (again & 31);
     if (orw < rows) {
       const int unit = (int)(e - (127.0f + kUp));
       const int otok = orw / group;
@@ -737,12 +858,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 16; r += 4) {
-          const int d = 32 * n + 2 * r + 4 * lh;
+          const int d = 32 * n + 2 * r + 4 * oh;
           const v4f o = scaled4(v4f{acc[n][r], acc[n][r + 1], acc[n][r + 2], acc[n][r + 3]} * inv, unit);
           if (splits > 1) *(v4f*)(a.part + ((int64_t)split * kv.tokens * a.heads + orow) * D + d) = o;
           else *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
         }
-      if (lh == 0) {
+      if (__builtin_expect(careful, 0)) put_nan<D>(a, s, head, orow, sp.past + otok, split, splits > 1, kb0, kb1, block_lo, block_hi, 4 * oh, 8);
+      if (oh == 0) {
         if (splits > 1) {
           float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
           ml[0] = m;
@@ -752,6 +874,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
         }
       }
     }
+    careful = false;
+    tile -= row_tiles;
   }
 }
 
