@@ -57,3 +57,33 @@ def test_nan_value_codes(news, lens, Hq, Hk, D, page, window, causal, dt):
         assert torch.equal(torch.isnan(out), torch.isnan(want)), at
         assert torch.equal(out.nan_to_num(), want.nan_to_num()), at
         assert torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("news,lens,Hq,Hk,D,page,window", SHAPES)
+def test_nan_scores(news, lens, Hq, Hk, D, page, window):
+    """A key or a query with a NaN: outputs and log-sum-exp of the rows that see it are NaN, not 'no key'."""
+    rng = np.random.default_rng(sum(lens) + D + 1)
+    table, pages = table_of(rng, lens, page)
+    cache = random_cache(rng, pages, Hk, page, D)
+    start, batch = batch_of(news, lens, table)
+    q = torch.from_numpy(rng.standard_normal((int(start[-1]), Hq, D)).astype(np.float32)).to(BF).to(DEV)
+    clean, clean_lse = q8.q8_attention_kv8(q, device(cache), batch, window=window, lse=True)
+    assert torch.equal(torch.isneginf(clean_lse), (clean == 0).all(2))
+    n, total = news[0], lens[0]
+    at = total - 1 if n == 1 else total - max(1, min(n, total) // 2)
+    c = {**cache, "k": cache["k"].copy()}
+    c["k"][table[0, at // page], 0, at % page, D - 2] = 0x7F
+    out, lse = q8.q8_attention_kv8(q, device(c), batch, window=window, lse=True)
+    pos = total - n + np.arange(n)
+    rows = np.flatnonzero((at <= pos) & ((at > pos - window) if window else True))
+    bad = torch.zeros(clean_lse.shape, dtype=torch.bool)
+    bad[torch.from_numpy(rows), :Hq // Hk] = True
+    bad = bad.to(DEV)
+    assert len(rows) and out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+    x = q.clone()
+    x[-1, Hq - 1, 0] = float("nan")
+    out, lse = q8.q8_attention_kv8(x, device(cache), batch, window=window, lse=True)
+    assert out[-1, Hq - 1].isnan().all() and lse[-1, Hq - 1].isnan()
+    out[-1, Hq - 1], lse[-1, Hq - 1] = clean[-1, Hq - 1], clean_lse[-1, Hq - 1]
+    assert torch.equal(out, clean) and torch.equal(lse, clean_lse)

@@ -401,7 +401,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
       }
       const int otok = orw / group, oh = orw - otok * group;
       const int64_t orow = (int64_t)(sp.first + otok) * a.heads + head * group + oh;
-      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) {
         const int d = part * 4 + e * 64;
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
           ml[0] = mm;
           ml[1] = ll;
         } else if (a.lse) {
-          a.lse[orow] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -INFINITY;
+          a.lse[orow] = ll == 0.0f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f;
         }
       }
     }
@@ -853,7 +853,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
       const int unit = (int)(e - (127.0f + kUp));
       const int otok = orw / group;
       const int64_t orow = (int64_t)(sp.first + otok) * a.heads + head * group + (orw - otok * group);
-      const float inv = splits > 1 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
+      const float inv = splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -870,7 +870,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
           ml[0] = m;
           ml[1] = l;
         } else if (a.lse) {
-          a.lse[orow] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
+          a.lse[orow] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
         }
       }
     }
@@ -922,14 +922,14 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks,
     for (int i = g; i < splits; i += G) o += *(const v4f*)(a.part + (i * rows + row) * D + d) * s_f[i];
     *(v4f*)&s_o[g][d] = o;
     __syncthreads();
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
     if (tid < D) {
       float v = s_o[0][tid];
 #pragma unroll
       for (int i = 1; i < G; ++i) v += s_o[i][tid];
       store_out<DT>(a.out, row * D + tid, v * inv);
     }
-    if (a.lse && tid == 0) a.lse[row] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -INFINITY;
+    if (a.lse && tid == 0) a.lse[row] = ll == 0.0f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f;
   }
 }
 
