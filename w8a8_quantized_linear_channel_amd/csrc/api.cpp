@@ -697,9 +697,6 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
   a.rot = rotate ? (int)rot_dim : 0;
   a.interleaved = interleaved != 0;
   const int64_t mq = bound_of(max_q, T);
-  int64_t reach = (mq + page - 2) / page + 1;        // pages that mq tokens can lie in
-  reach = reach > max_pages ? max_pages : reach;
-  a.reach = (int)reach;
   a.max_q = (int)mq;
   return launched(q8::launch_kv_append(a, dtype, (int)D, st));
 }

@@ -18,6 +18,7 @@
 // sequence, 6.2 for 128).
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
+#include "q8_kv_plan.hpp"
 
 namespace q8 {
 namespace {
@@ -452,24 +453,22 @@ __global__ __launch_bounds__((Shape<DT, D, B>::kThreads), 4) void k_kv_append(co
 template <int DT, int D, int B>
 hipError_t launch_shape(const AppendArgs& a, hipStream_t st) {
   using SH = Shape<DT, D, B>;
-  const int64_t groups = (2 * a.kv.kv_heads + SH::kItems - 1) / SH::kItems;
-  // one new token each: lanes by head and features instead of patches, of which it would fill one lane
-  // in B / kPatch
-  const int64_t token_blocks = a.max_q == 1 ? ((int64_t)2 * a.kv.kv_heads * (D / 8) + SH::kThreads - 1) / SH::kThreads : 0;
-  const int64_t kv_blocks = token_blocks > 0 ? a.kv.seqs * token_blocks : (int64_t)a.kv.seqs * a.reach * groups;
-  int64_t q_blocks = 0;
-  // heads of a thread: one where there are few tokens (latency), eight that share their angles elsewhere
-  const int span = (int64_t)a.max_q * a.kv.seqs >= 1024 ? 8 : 1;
-  if (a.q) {
-    const int64_t units = D / 8 - (a.interleaved ? 0 : a.rot >> 4), spans = (a.heads + span - 1) / span;
-    q_blocks = ((int64_t)a.max_q * units * spans + SH::kThreads - 1) / SH::kThreads;
-    const int64_t most = ((int64_t)1 << 30) / a.kv.seqs;
-    q_blocks = q_blocks > most ? most : q_blocks;
+  const int units = a.q ? D / 8 - (a.interleaved ? 0 : a.rot >> 4) : 0;
+  const AppendPlan p = append_plan(a.kv.seqs, a.max_q, a.kv.max_pages, B, a.kv.kv_heads, D, a.heads, units, SH::kItems, SH::kThreads);
+  AppendArgs part = a;
+  part.reach = (int)p.reach;
+  for (int s = 0; s < a.kv.seqs; s += p.seqs) {
+    part.kv.seqs = a.kv.seqs - s < p.seqs ? a.kv.seqs - s : p.seqs;
+    part.kv.q_start = a.kv.q_start + s;
+    part.kv.kv_len = a.kv.kv_len + s;
+    part.kv.table = a.kv.table + (int64_t)s * a.kv.max_pages;
+    const int64_t kv_blocks = p.kv_blocks(part.kv.seqs);
+    k_kv_append<DT, D, B><<<(unsigned)(kv_blocks + p.q_blocks * part.kv.seqs), SH::kThreads, 0, st>>>(
+        part, (int)kv_blocks, (int)p.groups, p.q_blocks > 0 ? (int)p.q_blocks : 1, p.span, (int)p.token_blocks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (kv_blocks + q_blocks * a.kv.seqs > ((int64_t)1 << 31) - 1) return hipErrorInvalidValue;
-  k_kv_append<DT, D, B><<<(unsigned)(kv_blocks + q_blocks * a.kv.seqs), SH::kThreads, 0, st>>>(
-      a, (int)kv_blocks, (int)groups, q_blocks > 0 ? (int)q_blocks : 1, span, (int)token_blocks);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 template <int DT, int D>

@@ -35,13 +35,13 @@
 
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
+#include "q8_kv_plan.hpp"
 
 namespace q8 {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 64;      // keys of one wave step
 
 template <int DT>
 __device__ __forceinline__ v4f mma16(const v4i a, const v4i b, const v4f c) {
@@ -453,7 +453,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
 // 1.2); its MFMAs alone take 465 us, with the LDS reads of their operands 494.
 // Two workgroups of 4 waves a CU 775 us, halves of the waves in turns 766.
 typedef float v16 __attribute__((ext_vector_type(16)));
-constexpr int kStep = 64;        // keys of one step
 constexpr int kMeta = 256;       // 32-key halves whose page and exponents are held at a time
 
 template <int DT>
@@ -884,7 +883,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
 // groups through LDS; always in the same order.  Bound by the partial sums' bytes
 // and a launch (a row by less than a workgroup: 15 against 7 us for 64 rows of
 // 128 features in 59 splits).
-constexpr int kMaxSplits = 256;
 template <int D, int DT>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks, int splits) {
   constexpr int G = 1024 / D;
@@ -933,80 +931,10 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks,
   }
 }
 
-constexpr int kSmallRows = 16;      // of a workgroup where there are few rows
-
-// How a call is cut: rows of one workgroup, row blocks of a sequence, splits of the keys and keys of
-// one split.
-struct Plan {
-  int64_t per, blocks;
-  int splits, chunk;
-};
-Plan plan_of(int64_t rows, int dim, int kv_heads, int seqs, int64_t max_q, int64_t max_kv, int window) {
-  Plan p;
-  const int64_t pairs = (int64_t)seqs * kv_heads;
-  int64_t seen = max_kv;
-  if (window > 0 && window + max_q < seen) seen = window + max_q;
-  // Few rows, 16 a workgroup: up to 64, and up to 128 where the blocks of 16 together read no more than
-  // half a million keys (8 kv heads of 128 features, this way against many rows': 24 rows on 300 keys
-  // 7.7 against 13.7 us, 64 on 110000 127 against 131, 32 sequences of 64 on 2000 64 against 77, 8 of 128
-  // on 300 12 against 21, one of 128 on 16000 42 against 34).  256 features, one wave a SIMD and half the
-  // bytes in flight: beyond 16 rows only up to a quarter of a million (2 sequences of 128 on 2000 30
-  // against 38, of 64 on 10000 76 against 49).
-  const bool few = rows <= kSmallRows || (dim < 256 && rows <= 64) ||
-                   (rows <= 128 && pairs * ((rows + kSmallRows - 1) / kSmallRows) * seen <=
-                                       (int64_t)1 << (dim < 256 ? 19 : 18));
-  // Many rows: 8 waves (two on a SIMD) share a step's codes; 4 at 256 features, whose accumulators,
-  // queries and scores fit a wave only where it has the SIMD's registers to itself, and at 64 features
-  // where blocks of 256 rows would leave CUs without one.
-  p.per = few ? kSmallRows
-          : dim == 256 || (dim == 64 && pairs * ((rows + 255) / 256) < 256) ? 128 : 256;
-  p.blocks = (rows + p.per - 1) / p.per;
-  const int64_t groups = pairs * p.blocks;
-  // keys that a workgroup's rows see
-  const int64_t block_q = p.blocks > 1 ? p.per * max_q / rows + 2 : max_q;
-  int64_t keys = max_kv;
-  if (window > 0 && window + block_q + 2 * kTile < keys) keys = window + block_q + 2 * kTile;
-  int64_t want, least;      // splits, and keys of one
-  if (p.per == kSmallRows) {
-    // Splits to fill the chip, none where the sequences and heads do it alone (64 sequences, 8 kv heads,
-    // up to 4099 keys: 74 us whole, 77 + 5 in 1024-key shares), but none longer than 8192 keys either,
-    // so that one long sequence among many does not hold up the rest.  A share under 1024 keys costs
-    // the join more than it saves.
-    want = groups >= 512 ? 1 : 1024 / groups;
-    if (want < keys / 8192) want = keys / 8192;
-    least = 1024;
-  } else {
-    // As many as give every CU a workgroup, where the steps that they take off the longest one are worth
-    // the join: its launch and the partial sums that it writes and reads back (32-bit, at some 4.5 TB/s).
-    // One sequence, 32 heads, 8 kv heads, 128 features, 512 new tokens on 8192: 4 splits 102 us, 8 splits
-    // 113; 5 sequences, 8 heads of each, 28 on 920: 6 splits 18 us, none 34; 5 sequences, 4 heads of
-    // each, 576 on 61, window 256: 4 splits 36 us, none 31.
-    const double step_us = (double)(kStep * p.per * dim) / (64 * 256 * 128) * 1.8;
-    const double whole = (double)keys / kStep * step_us, unit = (double)pairs * (double)rows * dim * 8 / 4.5e6;
-    want = 256 / groups;
-    const int64_t worth = (int64_t)__builtin_sqrt(whole / unit);
-    want = want > worth ? worth : want;
-    if (want > 1 && whole / want + 5.0 + unit * want > whole) want = 1;
-    least = 128;
-  }
-  want = want > kMaxSplits ? kMaxSplits : want;
-  want = want < 1 ? 1 : want;
-  int64_t c = ((keys + want - 1) / want + least / 2 - 1) / (least / 2) * (least / 2);
-  c = c < least ? least : c;
-  p.splits = (int)((keys + c - 1) / c);
-  if (p.splits < 1) p.splits = 1;
-  p.chunk = (int)c;
-  if (few && p.blocks > 65535 / seqs) p.blocks = 65535 / seqs;
-  const int64_t most_blocks = ((int64_t)1 << 30) / (pairs * p.splits);
-  if (p.blocks > most_blocks) p.blocks = most_blocks;
-  if (p.blocks < 1) p.blocks = 1;
-  return p;
-}
-
 template <int D, int DT>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.heads / a.kv.kv_heads);
-  const Plan p = plan_of(rows, D, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
+  const AttnPlan p = attn_plan(rows, D, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
   const int blocks = (int)p.blocks;
   if (p.per == kSmallRows) {
     const dim3 grid((unsigned)p.splits, (unsigned)a.kv.kv_heads, (unsigned)(p.blocks * a.kv.seqs));
@@ -1026,9 +954,7 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  int64_t jb = (int64_t)a.max_q * a.heads;
-  const int64_t limit = ((int64_t)1 << 30) / a.kv.seqs;
-  jb = jb > limit ? limit : jb;
+  const int64_t jb = join_blocks(a.max_q, a.heads, a.kv.seqs);
   k_attn_join<D, DT><<<(unsigned)(jb * a.kv.seqs), 256, 0, st>>>(a, (int)jb, p.splits);
   return hipGetLastError();
 }
@@ -1044,7 +970,7 @@ hipError_t launch_dt(const AttnArgs& a, int dim, hipStream_t st) {
 }  // namespace
 
 int attn_splits(int heads, int kv_heads, int dim, int seqs, int64_t max_q, int64_t max_kv, int window) {
-  return plan_of(max_q * (heads / kv_heads), dim, kv_heads, seqs, max_q, max_kv, window).splits;
+  return attn_plan(max_q * (heads / kv_heads), dim, kv_heads, seqs, max_q, max_kv, window).splits;
 }
 
 hipError_t launch_attention(const AttnArgs& a, int dt, int dim, hipStream_t st) {

@@ -27,7 +27,7 @@ struct AppendArgs {
   int heads;
   const float *cos, *sin;          // [positions, rot / 2]
   int positions, rot, interleaved;
-  int reach;                       // grid extent over the pages one sequence's new tokens touch
+  int reach;                       // grid extent over the pages one sequence's new tokens touch (the launcher's)
   int max_q;
 };
 hipError_t launch_kv_append(const AppendArgs& a, int dt, int dim, hipStream_t st);
