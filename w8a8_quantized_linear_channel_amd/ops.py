@@ -55,7 +55,11 @@ def q8_workspace_bytes(op: str, M: int, N: int, K: int) -> int:
     return int(_lib.lib().q8_workspace_bytes(_OP[op], M, N, K))
 
 
-def _workspace(op: str, M: int, N: int, K: int, dev) -> torch.Tensor:
+def _workspace(op: str, M: int, N: int, K: int, dev, given: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The caller's workspace, checked (the call checks its size), or one of the size that the call needs."""
+    if given is not None:
+        _need(given, "workspace", None, None, dev)
+        return given
     n = q8_workspace_bytes(op, M, N, K)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
 
@@ -129,9 +133,9 @@ def q8_linear(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, w_zp: to
     y = out if out is not None else torch.empty(M, N, dtype=out_dtype, device=dev)
     _need(y, "y", out_dtype, (M, N), dev)
     acc = torch.empty(M, N, dtype=torch.int32, device=dev) if acc_out else None
-    ws = workspace if workspace is not None else _workspace("linear", M, N, K, dev)
+    ws = _workspace("linear", M, N, K, dev, workspace)
     st = _lib.lib().q8_linear(_ptr(x), _DT[x.dtype], M, K, _ptr(wq), _ptr(w_scale), _ptr(w_zp), N,
-                              _ptr(bias), _ptr(y), _DT[out_dtype], _ptr(ws), ws.numel(), _ptr(acc),
+                              _ptr(bias), _ptr(y), _DT[out_dtype], _ptr(ws), ws.nbytes, _ptr(acc),
                               _stream(dev))
     _lib.check("q8_linear", st)
     return (y, acc) if acc_out else y
@@ -183,9 +187,9 @@ def q8_linear_int8_decomp(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tens
     idx = torch.empty(K, dtype=torch.int32, device=dev) if return_outliers else None
     cnt = torch.empty(1, dtype=torch.int32, device=dev) if return_outliers else None
     acc = torch.empty(M, N, dtype=torch.int32, device=dev) if acc_out else None
-    ws = workspace if workspace is not None else _workspace("decomp", M, N, K, dev)
+    ws = _workspace("decomp", M, N, K, dev, workspace)
     st = _lib.lib().q8_linear_int8_decomp(_ptr(x), M, K, _ptr(wq), _ptr(w_scale), _ptr(w_zp), N,
-                                          float(threshold), _ptr(bias), _ptr(y), _ptr(ws), ws.numel(),
+                                          float(threshold), _ptr(bias), _ptr(y), _ptr(ws), ws.nbytes,
                                           _ptr(idx), _ptr(cnt), _ptr(acc), _stream(dev))
     _lib.check("q8_linear_int8_decomp", st)
     res = [y]
@@ -210,9 +214,9 @@ def q8_linear_fp8(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
         _need(bias, "bias", torch.float32, (N,), dev)
     y = out if out is not None else torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     _need(y, "y", torch.bfloat16, (M, N), dev)
-    ws = workspace if workspace is not None else _workspace("fp8", M, N, K, dev)
+    ws = _workspace("fp8", M, N, K, dev, workspace)
     st = _lib.lib().q8_linear_fp8(_ptr(x), M, K, _ptr(wq), _ptr(w_scale), N, float(scale_ub), _ptr(bias),
-                                  _ptr(y), _ptr(ws), ws.numel(), _stream(dev))
+                                  _ptr(y), _ptr(ws), ws.nbytes, _stream(dev))
     _lib.check("q8_linear_fp8", st)
     return y
 
@@ -317,10 +321,10 @@ def q8_linear_static(x: torch.Tensor, x_scale: float, wq: torch.Tensor, w_scale:
         _need(bias, "bias", torch.float32, (N,), dev)
     yq = out if out is not None else torch.empty(M, N, dtype=torch.int8, device=dev)
     _need(yq, "yq", torch.int8, (M, N), dev)
-    ws = workspace if workspace is not None else _workspace("static", M, N, K, dev)
+    ws = _workspace("static", M, N, K, dev, workspace)
     st = _lib.lib().q8_linear_static(_ptr(x), _DT[x.dtype], M, K, float(x_scale), _ptr(wq), _ptr(w_scale),
                                      _ptr(w_zp), N, _ptr(bias), float(y_scale), _ptr(yq), _ptr(ws),
-                                     ws.numel(), _stream(dev))
+                                     ws.nbytes, _stream(dev))
     _lib.check("q8_linear_static", st)
     return yq
 
@@ -339,9 +343,9 @@ def q8_linear_fp8_grouped(x: torch.Tensor, expert_offsets: torch.Tensor, wq: tor
     _need(w_scale, "w_scale", torch.float32, (E, N), dev)
     y = out if out is not None else torch.empty(T, N, dtype=torch.bfloat16, device=dev)
     _need(y, "y", torch.bfloat16, (T, N), dev)
-    ws = workspace if workspace is not None else _workspace("fp8", T, N, K, dev)
+    ws = _workspace("fp8", T, N, K, dev, workspace)
     st = _lib.lib().q8_linear_fp8_grouped(_ptr(x), T, K, _ptr(expert_offsets), E, _ptr(wq), _ptr(w_scale), N,
-                                          float(scale_ub), _ptr(y), _ptr(ws), ws.numel(), _stream(dev))
+                                          float(scale_ub), _ptr(y), _ptr(ws), ws.nbytes, _stream(dev))
     _lib.check("q8_linear_fp8_grouped", st)
     return y
 
@@ -382,9 +386,9 @@ def q8_linear_grouped(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, 
         _need(bias, "bias", torch.float32, (N,), dev)
     y = out if out is not None else torch.empty(M, N, dtype=out_dtype, device=dev)
     _need(y, "y", out_dtype, (M, N), dev)
-    ws = workspace if workspace is not None else _workspace("grouped", M, N, K, dev)
+    ws = _workspace("grouped", M, N, K, dev, workspace)
     st = _lib.lib().q8_linear_grouped(_ptr(x), _DT[x.dtype], M, K, _ptr(wq), _ptr(w_scale), _ptr(w_zp), group, N,
-                                      _ptr(bias), _ptr(y), _DT[out_dtype], _ptr(ws), ws.numel(), _stream(dev))
+                                      _ptr(bias), _ptr(y), _DT[out_dtype], _ptr(ws), ws.nbytes, _stream(dev))
     _lib.check("q8_linear_grouped", st)
     return y
 
@@ -600,7 +604,7 @@ def q8_attention_kv8(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Opt
         if wsn:
             ws = torch.empty(wsn, dtype=torch.uint8, device=dev)
     else:
-        wsn = ws.numel() * ws.element_size()
+        wsn = ws.nbytes
         if ws.get_device() != index or not ws.is_contiguous():
             _need(ws, "workspace", None, None, dev)
     st = L.q8_attention_kv8(q.data_ptr(), q_step, _DT[dt], T, Hq, Hkv, D, batch.q_start.data_ptr(),
@@ -704,7 +708,8 @@ def q8_linear_fp8_block(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor
         if wsn:
             ws = torch.empty(wsn, dtype=torch.uint8, device=dev)
     else:
-        wsn = ws.numel()
+        _need(ws, "workspace", None, None, dev)
+        wsn = ws.nbytes
     st = L.q8_linear_fp8_block(x.data_ptr(), _DT[xd], M, K, wq.data_ptr(), w_scale.data_ptr(), N, _ptr(bias),
                                y.data_ptr(), _DT[out_dtype], _ptr(ws), wsn, _raw_stream(index))
     if st:
