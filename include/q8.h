@@ -451,6 +451,8 @@ size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t 
  *     S = max(max |.| over the block / 448, 1e-8),  q = e4m3_rne(clamp(. / S, -448, 448))
  * w: [N, K], wq: uint8 [N, K], w_scale: float [ceil(N / 128), G].
  * x: [M, K], xq: uint8 [M, K], x_scale: float [G, M] (block-major).
+ * A NaN or an infinity makes its block's S one, and what is computed from the
+ * block is not finite (NaN for a NaN).
  * w, x of type F32, F16 or BF16.
  */
 q8_status q8_quantize_weight_block(const void* w, q8_dtype w_dtype, int64_t N, int64_t K,

@@ -25,6 +25,12 @@ __device__ __forceinline__ void load8(const void* base, int64_t off, float* v) {
   }
 }
 
+// max(a, |b|), a NaN if either is: a block with a NaN gets a NaN scale, so that what is computed from it
+// is NaN, too (the clamp of the codes would make -448 of it)
+__device__ __forceinline__ float amax_of(float a, float b) { return __builtin_elementwise_maximum(a, fabsf(b)); }
+// of non-negative floats or NaN, whose bit patterns order as integers
+__device__ __forceinline__ int bits_max(int a, int b) { return a > b ? a : b; }
+
 // e4m3 codes of 8 values, x / s rounded as the correctly rounded quotient is
 // (16-bit inputs: two FMAs on RN(1/s), the same codes over that whole domain)
 template <int DT>
@@ -51,10 +57,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_act_block(const void* __rest
   if (k < K) load8<DT>(x, m * K + k, v);
   float amax = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
-  amax = __int_as_float(dpp_row_reduce(__float_as_int(amax), [](int a, int b) {
-    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
-  }));
+  for (int e = 0; e < 8; ++e) amax = amax_of(amax, v[e]);
+  amax = __int_as_float(dpp_row_reduce(__float_as_int(fabsf(amax)), bits_max));
   float s = amax / kFp8Max;
   s = s < kEps ? kEps : s;
   if (k < K) *(v2i*)(xq + m * K + k) = codes8<DT>(v, s);
@@ -65,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_act_block(const void* __rest
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_quant_weight_block(const void* __restrict__ w, int64_t N, int64_t K,
                                                                  uint8_t* __restrict__ wq, float* __restrict__ w_scale) {
-  __shared__ float red[kThreads / 64];
+  __shared__ int red[kThreads / 64];
   const int cols = (int)((K + kScaleBlock - 1) / kScaleBlock);
   const int64_t n0 = (int64_t)(blockIdx.x / cols) * kScaleBlock;
   const int k = (int)(blockIdx.x % cols) * kScaleBlock + 8 * (threadIdx.x & 15);
@@ -76,9 +80,16 @@ __global__ __launch_bounds__(kThreads) void k_quant_weight_block(const void* __r
     float v[8];
     load8<DT>(w, (n0 + r) * K + k, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    for (int e = 0; e < 8; ++e) amax = amax_of(amax, v[e]);
   }
-  amax = block_max<kThreads / 64>(amax, red);
+  int top = dpp_row_reduce(__float_as_int(fabsf(amax)), bits_max);
+  top = bits_max(bits_max(__builtin_amdgcn_readlane(top, 0), __builtin_amdgcn_readlane(top, 16)),
+                 bits_max(__builtin_amdgcn_readlane(top, 32), __builtin_amdgcn_readlane(top, 48)));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) top = bits_max(top, red[w]);
+  amax = __int_as_float(top);
   float s = amax / kFp8Max;
   s = s < kEps ? kEps : s;
   for (int r = r0; r < kScaleBlock; r += kThreads / 16) {
@@ -623,14 +634,13 @@ __global__ __launch_bounds__(kThreads) void k_gemv_block_fused(const void* __res
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           v[e] = inx ? v[e] : 0.0f;
-          amax = fmaxf(amax, fabsf(v[e]));
+          amax = amax_of(amax, v[e]);
         }
         // over the block's 8 lanes: pairs, pairs of pairs, the half-row's two quads
-        int am = __float_as_int(amax);
-        auto up = [](int a, int b) { return a > b ? a : b; };     // of non-negative floats
-        am = up(am, __builtin_amdgcn_update_dpp(0, am, 0xB1, 0xF, 0xF, false));
-        am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x4E, 0xF, 0xF, false));
-        am = up(am, __builtin_amdgcn_update_dpp(0, am, 0x141, 0xF, 0xF, false));
+        int am = __float_as_int(fabsf(amax));
+        am = bits_max(am, __builtin_amdgcn_update_dpp(0, am, 0xB1, 0xF, 0xF, false));
+        am = bits_max(am, __builtin_amdgcn_update_dpp(0, am, 0x4E, 0xF, 0xF, false));
+        am = bits_max(am, __builtin_amdgcn_update_dpp(0, am, 0x141, 0xF, 0xF, false));
         float s = __int_as_float(am) / kFp8Max;
         s = s < kEps ? kEps : s;
         const v2i lo = codes8<XDT>(v, s), hi = codes8<XDT>(v + 8, s);
