@@ -194,13 +194,14 @@ PyObject* linear_fp8_block(PyObject* const* a) {
     yd = reinterpret_cast<THPDtype*>(a[4])->scalar_type;
   }
   const int xc = dtype_code(xd), yc = dtype_code(yd);
-  if (xc < 0 || yc < 0 || !x->is_contiguous() || !dense(*wq, at::kByte, {N, K}, dev) ||
+  if (xc < 0 || yc < 0 || !x->is_contiguous() || !one_byte(wq->scalar_type(), at::kFloat8_e4m3fn) ||
+      !dense(*wq, wq->scalar_type(), {N, K}, dev) ||
       !dense(*ws, at::kFloat, {(N + 127) / 128, (K + 127) / 128}, dev) || (bias && !dense(*bias, at::kFloat, {N}, dev)) ||
       (out && !dense(*out, yd, {M, N}, dev)))
     return not_ours();
   at::Tensor y = out ? *out : at::empty({M, N}, x->options().dtype(yd)), scratch;
   const size_t need = q8_workspace_bytes(Q8_OP_FP8_BLOCK, M, N, K);
-  if (need) scratch = at::empty({(int64_t)need}, wq->options());
+  if (need) scratch = at::empty({(int64_t)need}, wq->options().dtype(at::kByte));
   void* st;
   if (!stream_of(dev, &st)) return nullptr;
   const q8_status s = q8_linear_fp8_block(ptr(x), (q8_dtype)xc, M, K, (const uint8_t*)ptr(wq), (const float*)ptr(ws), N,

@@ -425,7 +425,7 @@ def q8_kv_cache(num_pages: int, kv_heads: int, head_dim: int, page: int = 64, de
                    z(num_pages, kv_heads, head_dim, page), z(num_pages, kv_heads))
 
 
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+_CODES = (torch.uint8, torch.float8_e4m3fn)      # of e4m3 codes
 _EXPS = (torch.uint8, torch.float8_e8m0fnu)
 _I32 = torch.int32
 
@@ -617,6 +617,12 @@ def q8_attention_kv8(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Opt
     return (y, le) if lse else y
 
 
+def _need_codes(t: torch.Tensor, name: str, shape=None, dev=None) -> None:
+    _need(t, name, None, shape, dev)
+    if t.dtype not in _CODES:
+        raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
+
+
 def q8_quantize_weight_block(w: torch.Tensor):
     """FP8 weights with one scale per 128 x 128 block: (wq uint8 e4m3 codes [N, K],
     w_scale float32 [ceil(N/128), ceil(K/128)])."""
@@ -653,14 +659,15 @@ def q8_quantize_act_block(x: torch.Tensor, out=None):
 def q8_gemm_fp8_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
                       bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                       out: Optional[torch.Tensor] = None):
-    """The block-scaled FP8 product on quantized operands (bf16 or fp16 out)."""
-    _need(xq, "xq", torch.uint8)
+    """The block-scaled FP8 product on quantized operands, codes as uint8 or
+    float8_e4m3fn (bf16 or fp16 out)."""
+    _need_codes(xq, "xq")
     dev = xq.device
     M, K = xq.shape
     N = wq.shape[0]
     G = -(-K // 128)
     _need(x_scale, "x_scale", torch.float32, (G, M), dev)
-    _need(wq, "wq", torch.uint8, (N, K), dev)
+    _need_codes(wq, "wq", (N, K), dev)
     _need(w_scale, "w_scale", torch.float32, (-(-N // 128), G), dev)
     if bias is not None:
         _need(bias, "bias", torch.float32, (N,), dev)
@@ -675,8 +682,8 @@ def q8_gemm_fp8_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
 def q8_linear_fp8_block(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
                         bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
-    """Linear layer with block-scaled FP8 weights (from q8_quantize_weight_block)
-    and activations quantized per token and 128 features; bf16 or fp16 out
+    """Linear layer with block-scaled FP8 weights (from q8_quantize_weight_block,
+    or a checkpoint's float8_e4m3fn codes and scales) and activations quantized per token and 128 features; bf16 or fp16 out
     (default: x's dtype, bf16 for a float32 x)."""
     if workspace is None:
         r = _fast().linear_fp8_block(x, wq, w_scale, bias, out_dtype, out)
@@ -689,10 +696,10 @@ def q8_linear_fp8_block(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor
     N = wq.shape[0]
     xd = x.dtype
     blocks = (-(-N // 128), -(-K // 128))
-    if not (x.is_contiguous() and _is(wq, torch.uint8, (N, K), index) and _is(w_scale, torch.float32, blocks, index)
+    if not (x.is_contiguous() and wq.dtype in _CODES and _is(wq, wq.dtype, (N, K), index) and _is(w_scale, torch.float32, blocks, index)
             and (bias is None or _is(bias, torch.float32, (N,), index))):
         _need(x, "x")
-        _need(wq, "wq", torch.uint8, (N, K), dev)
+        _need_codes(wq, "wq", (N, K), dev)
         _need(w_scale, "w_scale", torch.float32, blocks, dev)
         _need(bias, "bias", torch.float32, (N,), dev)
     out_dtype = out_dtype or (torch.bfloat16 if xd is torch.float32 else xd)
