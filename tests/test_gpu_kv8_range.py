@@ -107,3 +107,14 @@ def test_values_of_zero_pages_and_extreme_exponents():
         cache["v"][table[0, 1:4]] = 0
         cache["ve"][table[0, 1:4]] = 0
         check_range(rng, [new], [400], 2, 1, 64, 32, BF, cache, table, 30.0)
+
+
+def test_reference_does_not_drift():
+    """Every fifth page far below the others: most steps move the rows' references, which must stay where the
+    largest term is over hundreds of them.  (The bound on the lengths keeps the keys in one share.)"""
+    rng = np.random.default_rng(9)
+    for new, D in ((100, 64), (100, 128), (4, 128)):
+        table, pages = table_of(rng, [6000], 32)
+        cache = random_cache(rng, pages, 1, 32, D)
+        cache["ve"][table[0, ::5]] = 96
+        check_range(rng, [new], [6000], 2, 1, D, 32, BF, cache, table, 20.0, max_kv=100)

@@ -21,12 +21,13 @@
 // exponent of a page multiplies the scores, the value exponent the softmax
 // weights (one factor of each per lane and tile: 32 keys lie in one page), so
 // value codes enter the product as they are.  What is rounded to f16 (2^-11 of
-// it) is p_j 2^(b_j - e), p_j = 2^(s_j - m): the weight of a key's codes, e a
-// whole number that each row holds beside its maximum m.  While every page that
-// a row sees has |b_j - e| <= gap, e stays and the exponent is part of the
-// exponential's argument; elsewhere e is moved so that the largest weight so far
-// is about 1 (a wave's slow step, with the softmax sum taken from exponentials
-// of its own).  Either way the row's largest weight is at least 2^-1 and none
+// it) is p_j 2^(b_j - e), p_j = 2^(s_j - m): the weight of a key's codes, m and
+// e whole numbers that each row holds (m its largest score so far, rounded down;
+// sums and differences of them are exact, so moving them leaves no drift).
+// While every page that a row sees has |b_j - e| <= gap, e stays and the exponent
+// is part of the exponential's argument; elsewhere e is moved so that the largest
+// weight so far is about 1 (a wave's slow step, with the softmax sum taken from
+// exponentials of its own).  Either way the row's largest weight is at least 2^-1 and none
 // passes 2^15, so what f16 cannot hold is below 2^-24 of the row's largest, and
 // pages that the row's mask hides do not enter at all.  Maximum, sum and
 // accumulator are held in 32 bits.
@@ -99,7 +100,7 @@ __device__ __forceinline__ void put_nan(const AttnArgs& a, int s, int head, int6
       key = all_hi - 1;
       continue;
     }
-    int p = kv.table[(int64_t)s * kv.max_pages + key / kv.page];
+    int p = kv.table[(int64_t)s * kv.max_pages + (key >> (31 - __builtin_clz(kv.page)))];
     p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
     const uint8_t* const v = kv.v + ((int64_t)p * kv.kv_heads + head) * D * kv.page + (key & (kv.page - 1));
 #pragma unroll 1
@@ -139,8 +140,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
   constexpr int KS = D / 32;        // MFMA steps over the features
   constexpr int KL = D / 64;        // 16-byte loads of a lane's share of a key
   constexpr int NT = D / 16;        // 16-feature tiles of the output
-  // weights p 2^(b - e + kUp), p <= 1: the largest from 2^(kUp - kGap) to 2^15
-  constexpr float kGap = 7.0f, kUp = 8.0f;
+  // weights p 2^(b - e + kUp), p < 2: the largest from 2^(kUp - kGap) to 2^15
+  constexpr float kGap = 7.0f, kUp = 7.0f;
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -259,20 +260,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
         }
       // over the row's four lanes; a lane without a visible key has no say about the exponents
       const bool seen = mx > -INFINITY;
-      const float own = mx + (float)vb;
+      const float own = ceilf(mx) + (float)vb;
       float gap = seen ? (float)vb - e : 0.0f;
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float mn = fmaxf(m, mx);
+      const float mn = fmaxf(m, floorf(mx));
       const float ref = mn == -INFINITY ? 0.0f : mn;
       const float alpha = __builtin_amdgcn_exp2f(m - ref);
       float fix = alpha, share = __builtin_amdgcn_exp2f(-(gap + kUp));
       l *= alpha;
       if (__any(fabsf(gap) > kGap)) {
-        // the largest weight so far, 2^top (that of the keys before to within the gap)
+        // the largest weight of this step is 2^top at most, that of the keys before 2^(m + e) to within the gap
         float top = fmaxf(own, __shfl_xor(own, 16));
-        top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m + e);
-        const float to = mn == -INFINITY ? e : ceilf(top - mn);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float to = mn == -INFINITY ? e : fmaxf(top - mn, e - (mn - m));
         fix = __builtin_amdgcn_exp2f(m - ref + (e - to));
         e = to;
         gap = seen ? (float)vb - e : 0.0f;
@@ -700,18 +701,19 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
       mx *= kscale;
       // a lane without a visible key has no say about the exponents
       const bool seen = mx > -INFINITY;
-      const float vb = (float)(exps >> 8), own = mx + vb;
+      const float vb = (float)(exps >> 8), own = ceilf(mx) + vb;
       float gap = seen ? vb - e : 0.0f;
       share = __builtin_amdgcn_exp2f(-(gap + kUp));
       if (__any(mx > m + 8.0f || fabsf(gap) > kGap)) {
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.0f : mn;
+        const float mn = fmaxf(m, floorf(mx)), ref = mn == -INFINITY ? 0.0f : mn;
         float fix = __builtin_amdgcn_exp2f(m - ref);
         l *= fix;
         if (__any(fabsf(gap) > kGap)) {
-          // the largest weight so far, 2^top (that of the keys before to within the gap)
-          const float top = fmaxf(fmaxf(own, __shfl_xor(own, 32)), m + e);
-          const float to = mn == -INFINITY ? e : ceilf(top - mn);
+          // the largest weight of this step is 2^top at most, that of the keys before 2^(m + e) to within
+          // the gap
+          const float top = fmaxf(own, __shfl_xor(own, 32));
+          const float to = mn == -INFINITY ? e : fmaxf(top - mn, e - (mn - m));
           fix = __builtin_amdgcn_exp2f(m - ref + (e - to));
           e = to;
           gap = seen ? vb - e : 0.0f;
