@@ -36,7 +36,7 @@ bool dense(const at::Tensor& t, at::ScalarType dt, at::IntArrayRef shape, int64_
 // [tokens, heads, dim], heads and features dense
 bool rows(const at::Tensor& t, at::ScalarType dt, int64_t heads, int64_t dim, int64_t dev) {
   return t.is_cuda() && t.get_device() == dev && t.scalar_type() == dt && t.dim() == 3 && t.size(1) == heads &&
-         t.size(2) == dim && (t.numel() == 0 || (t.stride(2) == 1 && t.stride(1) == dim));
+         t.size(2) == dim && (t.numel() == 0 || (t.stride(2) == 1 && (heads == 1 || t.stride(1) == dim)));
 }
 int dtype_code(at::ScalarType t) {
   switch (t) {

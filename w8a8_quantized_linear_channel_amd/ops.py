@@ -505,7 +505,7 @@ def _rows(t: torch.Tensor, name: str, dtype, tail, index: int) -> int:
     if t.dim() != 3 or t.shape[1:] != tail:
         raise ValueError(f"{name} must have shape [tokens, {tail[0]}, {tail[1]}], got {tuple(t.shape)}")
     step, heads, one = t.stride()
-    if (one != 1 or heads != tail[1]) and t.numel():
+    if (one != 1 or (heads != tail[1] and tail[0] > 1)) and t.numel():
         raise ValueError(f"{name} must have dense heads and features")
     return step
 
