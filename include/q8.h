@@ -415,9 +415,9 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
  * its sequence with j < kv_len, j <= p if causal, j > p - window if window > 0:
  *     w_j = softmax_j(scale q . k_j),   out = sum_j w_j v_j,   lse = log sum_j exp(scale q . k_j)
  * A query that sees no key gets out = 0 and lse = -inf, one with a NaN among the
- * scores that it sees NaN in both.  Codes of keys that a
- * query does not see have no part in its output, NaN codes included; pages that
- * no query sees need not exist.  Scores are exact products of codes and 16-bit queries.
+ * scores that it sees NaN in both.  Codes of keys that a query does not see have
+ * no part in its output, NaN codes included; pages that no query sees need not
+ * exist.  Scores are exact products of codes and 16-bit queries.
  * The weight of a key's value codes, w_j times its page's 2^(b - 127), is
  * rounded to f16 (2^-11 of it, or 2^-24 of the row's largest such weight where
  * that is more); its products with the codes are exact.  All sums, the maximum

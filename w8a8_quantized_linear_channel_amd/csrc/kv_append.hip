@@ -14,8 +14,8 @@
 //
 // Bound by bytes for prompts (350 MB, 105 us, 3.3 TB/s: the queries' copy runs
 // at a copy's rate, the keys and values wait for each page's maximum before the
-// first code leaves) and by latency for single tokens (3.6 us of kernel for one
-// sequence, 6.2 for 128).
+// first code leaves) and by latency for single tokens (3.8 us of kernel for one
+// sequence, 6.4 for 128, where no page's scale grows).
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
 #include "q8_kv_plan.hpp"

@@ -13,8 +13,8 @@
 // K and V go from memory to registers to MFMA without LDS, a tile's 8 D + 8 D
 // bytes all requested before the first is used: this is bound by the cache's
 // bytes (64 sequences of up to 4099 tokens, 32 heads over 8 of 128 features:
-// 313 MB in 74 us, 4.2 TB/s; 2 of 120000: 492 MB in 99 + 7 us to join 59 shares
-// of each, where a copy reaches 4.9 TB/s); one sequence of 513 keys takes 9.2
+// 313 MB in 75 us, 4.2 TB/s; 2 of 120000: 492 MB in 98 + 6 us to join 59 shares
+// of each, where a copy reaches 4.9 TB/s); one sequence of 513 keys takes 9.0
 // us, a chain of page table, exponents, codes and the waves' join.
 //
 // e4m3 codes convert to bf16 / f16 exactly (4 significant bits).  The key
@@ -27,10 +27,10 @@
 // While every page that a row sees has |b_j - e| <= gap, e stays and the exponent
 // is part of the exponential's argument; elsewhere e is moved so that the largest
 // weight so far is about 1 (a wave's slow step, with the softmax sum taken from
-// exponentials of its own).  Either way the row's largest weight is at least 2^-1 and none
-// passes 2^15, so what f16 cannot hold is below 2^-24 of the row's largest, and
-// pages that the row's mask hides do not enter at all.  Maximum, sum and
-// accumulator are held in 32 bits.
+// exponentials of its own).  Either way the row's largest weight is at least 2^-1
+// and none passes 2^15, so what f16 cannot hold is below 2^-24 of the row's
+// largest, and pages that the row's mask hides do not enter at all.  Maximum, sum
+// and accumulator are held in 32 bits.
 #include <type_traits>
 #include <utility>
 
@@ -42,7 +42,6 @@ namespace q8 {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
 
 template <int DT>
 __device__ __forceinline__ v4f mma16(const v4i a, const v4i b, const v4f c) {
@@ -67,6 +66,7 @@ __device__ __forceinline__ v4i widen8(int lo, int hi, float scale) {
                __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true))};
 }
 
+// v 2^e
 __device__ __forceinline__ v4f scaled4(const v4f v, int e) {
   return v4f{__builtin_ldexpf(v[0], e), __builtin_ldexpf(v[1], e), __builtin_ldexpf(v[2], e), __builtin_ldexpf(v[3], e)};
 }
@@ -450,9 +450,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
 // anything between lanes.
 //
 // Bound by the matrix units at the clock that the power leaves them: the prompt
-// of 8192 tokens is 550 G flop in 580 us, 0.95 PFLOP/s (a plain 8192^3 product
-// 1.2); its MFMAs alone take 465 us, with the LDS reads of their operands 494.
-// Two workgroups of 4 waves a CU 775 us, halves of the waves in turns 766.
+// of 8192 tokens is 550 G flop in 572 us once the clock has settled, 0.96
+// PFLOP/s, where a plain 8192^3 product reaches 1.45 (the first 20 launches after
+// a pause 655 us, and the product 1.25).  When the whole took 580 us its MFMAs
+// alone took 465, with the LDS reads of their operands 494.  Two workgroups of 4
+// waves a CU 775 us, halves of the waves in turns 766.
 typedef float v16 __attribute__((ext_vector_type(16)));
 constexpr int kMeta = 256;       // 32-key halves whose page and exponents are held at a time
 
@@ -528,7 +530,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     v4i qf[KS];
     {
       int qh = lh;
-      asm volatile("" : "+v"(qh));               // (nor need this)
+      asm volatile("" : "+v"(qh));               // (kept out of the loop's registers)
       const uint16_t* q = (const uint16_t*)a.q + (int64_t)(sp.first + tok) * a.q_stride +
                           (int64_t)(head * group + hq) * D + qh * (D / 2);
 #pragma unroll
