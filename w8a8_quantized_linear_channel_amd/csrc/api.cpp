@@ -171,7 +171,10 @@ q8_status check_kv(int64_t T, int64_t Hkv, int64_t D, int64_t S, int64_t max_pag
     return Q8_ERR_BAD_SHAPE;
   return Q8_OK;
 }
-bool valid_heads(int64_t Hq, int64_t Hkv) { return Hq >= 1 && Hq <= 65536 && Hq % Hkv == 0; }
+// (a sequence's rows, tokens x heads that share a kv head, are counted in 32 bits, a block past the end)
+bool valid_heads(int64_t T, int64_t Hq, int64_t Hkv) {
+  return Hq >= 1 && Hq <= 65536 && Hq % Hkv == 0 && T <= (kMaxRows - 1024) / (Hq / Hkv);
+}
 
 q8::KvView kv_view(const uint8_t* k, const uint8_t* ke, const uint8_t* v, const uint8_t* ve, const int32_t* q_start,
                    const int32_t* kv_len, const int32_t* table, int64_t T, int64_t Hkv, int64_t S, int64_t max_pages,
@@ -703,8 +706,8 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
 
 size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q,
                                     int64_t max_kv, int64_t window) {
-  if (check_kv(T, Hkv, D, S, 1, max_q, 1, 32) != Q8_OK || !valid_heads(Hq, Hkv) || max_kv < 0 || max_kv > kMaxRows ||
-      window < 0)
+  if (check_kv(T, Hkv, D, S, 1, max_q, 1, 32) != Q8_OK || !valid_heads(T, Hq, Hkv) || max_kv < 0 ||
+      max_kv > kMaxRows || window < 0)
     return 0;
   window = window > kMaxTokens ? 0 : window;
   return attn_ws(T, Hq, Hkv, D, S, bound_of(max_q, T), bound_of(max_kv, kMaxRows), window).total;
@@ -718,7 +721,7 @@ q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int6
                            void* workspace, size_t workspace_bytes, void* stream) {
   if (dtype != Q8_F16 && dtype != Q8_BF16) return Q8_ERR_BAD_DTYPE;
   Q8_TRY(check_kv(T, Hkv, D, S, max_pages, max_q, num_pages, page));
-  if (!valid_heads(Hq, Hkv) || max_kv < 0 || max_kv > kMaxRows) return Q8_ERR_BAD_SHAPE;
+  if (!valid_heads(T, Hq, Hkv) || max_kv < 0 || max_kv > kMaxRows) return Q8_ERR_BAD_SHAPE;
   if (T > 1 && (q_stride < Hq * D || q_stride % 8 != 0)) return Q8_ERR_BAD_SHAPE;
   if (!q_start || !kv_len || !block_table || !k_cache || !k_exp || !v_cache || !v_exp || (T > 0 && (!q || !out)))
     return Q8_ERR_NULL_PTR;
