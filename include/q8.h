@@ -410,6 +410,31 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
                        int64_t page, void* q_out, void* stream);
 
 /*
+ * q8_kv_append_norm -- q8_kv_append with each head of the new keys and queries
+ * normalised before it is rotated, and positions of the tokens' own.  A head x:
+ *     r = 1 / sqrt(sum_i x_i^2 / D + eps)   (sum and root in binary64, r rounded to binary32)
+ *     x_i -> (x_i r) w_i                    (binary32, each product rounded)
+ * then rotation and the append's rule as above.  Values are not normalised.
+ * q_weight, k_weight: [D] of w_dtype (F32, F16, BF16); NULL: that side is not
+ * normalised.  eps is positive and finite (ignored if both are NULL).
+ * token_positions: int32 [T] in device memory, the position that each token is
+ * rotated by (a drafted token's depth behind the cached ones, while its slot is
+ * its place among the new tokens), below 0 read as 0; NULL: its slot's.  The
+ * slots are q_start's and kv_len's in either case.
+ * Everything else is q8_kv_append's, with `positions` the rows of cos and sin.
+ */
+q8_status q8_kv_append_norm(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, q8_dtype dtype, int64_t T, int64_t Hq,
+                            int64_t Hkv, int64_t D, const void* q_weight, const void* k_weight,
+                            q8_dtype w_dtype, float eps, const float* cos, const float* sin,
+                            int64_t positions, int64_t rot_dim, int interleaved,
+                            const int32_t* token_positions, const int32_t* q_start,
+                            const int32_t* kv_len, const int32_t* block_table, int64_t S,
+                            int64_t max_pages, int64_t max_q, uint8_t* k_cache, uint8_t* k_exp,
+                            uint8_t* v_cache, uint8_t* v_exp, int64_t num_pages, int64_t page,
+                            void* q_out, void* stream);
+
+/*
  * q8_attention_kv8 -- softmax attention of the new queries over the cache.
  * Query token at position p, head h (reads kv head h / (Hq / Hkv)); keys j of
  * its sequence with j < kv_len, j <= p if causal, j > p - window if window > 0:
@@ -440,6 +465,105 @@ q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int6
  * which the call itself then rejects. */
 size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S,
                                     int64_t max_q, int64_t max_kv, int64_t window);
+
+/*
+ * q8_attention_kv8_tree -- q8_attention_kv8 where the new tokens of a sequence
+ * are drafts that continue each other as a tree (they lie in the cache already,
+ * put there by an append).  New token i of a sequence with n of them, `past` =
+ * kv_len - n cached before, sees
+ *     cached keys j < past, of them those with j > p - window if window > 0
+ *     new keys past + j with bit j % 64 of mask[t, j / 64] set (t = q_start + i; whatever the window)
+ * p: token_positions[t], taken within past .. past + n - 1; NULL: past + i.  A
+ * token sees itself only if its own bit is set; new keys without a bit in the
+ * row (j >= 64 mask_words) are not seen.
+ * mask: uint64 [T, mask_words] in device memory, 8-byte aligned; mask_words
+ * from 1 to 32768.  Everything else, a query that sees no key among it, is as
+ * q8_attention_kv8 has it.
+ * workspace: q8_attention_workspace_bytes(...) with the same sizes.
+ */
+q8_status q8_attention_kv8_tree(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T,
+                                int64_t Hq, int64_t Hkv, int64_t D, const int32_t* q_start,
+                                const int32_t* kv_len, const int32_t* block_table, int64_t S,
+                                int64_t max_pages, int64_t max_q, int64_t max_kv,
+                                const uint8_t* k_cache, const uint8_t* k_exp, const uint8_t* v_cache,
+                                const uint8_t* v_exp, int64_t num_pages, int64_t page,
+                                const uint64_t* mask, int64_t mask_words,
+                                const int32_t* token_positions, float scale, int64_t window,
+                                void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * Calls over the caches of all layers, which share one block table: k_cache,
+ * k_exp, v_cache and v_exp are arrays in HOST memory of `layers` device pointers
+ * (1 to 512, read before the call returns), no cache among them twice
+ * (Q8_ERR_BAD_ARG).
+ *
+ * q8_kv_compact -- the drafts of a batch that are kept go to the front of their
+ * slots, in place.  keep[s, i], i < n_keep[s]: the new token (0 .. n-1, as
+ * q_start numbers them) that becomes new token i of sequence s.  They grow
+ * (a path of a tree whose tokens follow the ones they continue); the list ends
+ * before an entry that does not, or is n or more.  Tokens with keep[s, i] = i at
+ * its front are in place.  The others, in slots p + keep[s, i] (p = kv_len - n),
+ * go to p + i by the append's rule, their values being what their codes stand
+ * for: each (page, kv head, tensor) that receives tokens:
+ *     want = least b >= 0 with max |moved values| <= 448 2^(b - 127)
+ *     b'   = want if the page's first slot receives one, else max(b, want)
+ *     slots before the first that receives one: codes c -> e4m3_rne(e4m3(c) 2^(b - b'))
+ *     a token from a page of byte u: code c -> e4m3_rne(e4m3(c) 2^(u - b')); NaN codes stay as they are
+ * Other slots keep their bytes (those behind the kept tokens are no longer
+ * read).  len_out[s] = p + the number kept.
+ * Tokens whose slot or target does not exist, or whose page number lies outside
+ * [0, num_pages), are not moved.  Two sequences must not share a page that one
+ * of them moves tokens in.
+ * keep: int32 [S, max_keep], n_keep, len_out: int32 [S], device memory; len_out
+ * overlaps no other array (Q8_ERR_BAD_ARG).  q_start, kv_len, block_table and
+ * the sizes as for q8_kv_append.  No workspace.
+ */
+q8_status q8_kv_compact(uint8_t* const* k_cache, uint8_t* const* k_exp, uint8_t* const* v_cache,
+                        uint8_t* const* v_exp, int64_t layers, int64_t Hkv, int64_t D,
+                        const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                        int64_t S, int64_t max_pages, int64_t num_pages, int64_t page,
+                        const int32_t* keep, int64_t max_keep, const int32_t* n_keep,
+                        int32_t* len_out, void* stream);
+
+/*
+ * q8_kv_fork -- a batch of S_out sequences that continue those of a batch of S:
+ * beams after a step, samples of a prompt, sequences that end, room for the next
+ * tokens.  refs[x] counts the block table entries that hold page x; 0: free.
+ * Sequence s of the new batch continues parent[s] (outside [0, S): it is empty
+ * and has no pages), L = kv_len[parent[s]] within [0, max_pages page] tokens:
+ *     entries j < L / page (full pages) are the parent's, shared
+ *     entries from there to (L + room) / page, rounded up, max_pages at most:
+ *       the parent's, if s is the first that continues it, it has one there and refs of it is 1;
+ *       else a new page, and if L ends inside it (j = L / page) the parent's page copied into it,
+ *       codes and exponent bytes, in every layer
+ *     further entries are -1
+ *     refs_out[x] = refs[x] - (entries of block_table that hold x) + (of table_out)
+ * Entries outside [0, num_pages) are none.  New pages are numbered by sequence
+ * and entry and are, in that order, the lowest pages that no entry holds any more
+ * (refs 0 once block_table's are let go and the shared and kept ones counted;
+ * pages that are copied from excepted).  missing[0] receives how many there were
+ * too few of: those entries are -1, and a sequence whose last tokens would be in
+ * one ends at the page before (len_out).  Else len_out[s] = L.
+ * The old table is let go as a whole: with parent = 0 .. S-1 a batch goes on as
+ * it is and gets its room, with fewer the others' pages are free afterwards.
+ * block_table: int32 [S, max_pages], kv_len: [S], refs: [num_pages], parent:
+ * [S_out]; table_out: [S_out, max_pages], len_out: [S_out], refs_out:
+ * [num_pages], missing: [1]; device memory, outputs and workspace overlap
+ * neither inputs nor each other (Q8_ERR_BAD_ARG).  room: 0 to 2^30; table_out has
+ * fewer than 2^31 entries.
+ * workspace: q8_kv_fork_workspace_bytes(S, S_out, num_pages) bytes.
+ */
+q8_status q8_kv_fork(uint8_t* const* k_cache, uint8_t* const* k_exp, uint8_t* const* v_cache,
+                     uint8_t* const* v_exp, int64_t layers, int64_t Hkv, int64_t D,
+                     int64_t num_pages, int64_t page, const int32_t* block_table,
+                     const int32_t* kv_len, const int32_t* refs, int64_t S, int64_t max_pages,
+                     const int32_t* parent, int64_t S_out, int64_t room, int32_t* table_out,
+                     int32_t* len_out, int32_t* refs_out, int32_t* missing, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace q8_kv_fork needs; 0 for invalid sizes. */
+size_t q8_kv_fork_workspace_bytes(int64_t S, int64_t S_out, int64_t num_pages);
 
 /*
  * Block-scaled FP8 linear: e4m3 codes with one scale per token and 128

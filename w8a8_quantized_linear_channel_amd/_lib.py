@@ -50,6 +50,14 @@ SIGNATURES = {
                             _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P]),
     "q8_attention_kv8": (_INT, [_P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64,
                                 _P, _P, _P, _P, _I64, _I64, _F, _INT, _I64, _P, _P, _P, _SZ, _P]),
+    "q8_kv_append_norm": (_INT, [_P, _I64, _P, _I64, _P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _P, _INT, _F, _P, _P,
+                                 _I64, _I64, _INT, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P]),
+    "q8_attention_kv8_tree": (_INT, [_P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64,
+                                     _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _F, _I64, _P, _P, _P, _SZ, _P]),
+    "q8_kv_compact": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P]),
+    "q8_kv_fork": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _P,
+                          _P, _P, _P, _SZ, _P]),
+    "q8_kv_fork_workspace_bytes": (_SZ, [_I64] * 3),
     "q8_attention_workspace_bytes": (_SZ, [_I64] * 8),
     "q8_quantize_weight_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
     "q8_quantize_act_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),

@@ -7,6 +7,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -24,6 +25,8 @@ constexpr int64_t kMaxK = 65536;          // keeps acc - Z*rowsum inside int32 (
 constexpr int64_t kMaxRows = (1LL << 31) - 1;
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxTokens = 1LL << 30;       // of one batch over the cache, and of a window
+constexpr int64_t kMaxMaskWords = 1 << 15;      // of a drafted token's mask (64 tokens each)
+constexpr int kMaxLayers = 512;                 // of one call over the caches of all layers
 constexpr int64_t kMaxGroups = 1024;            // experts of one grouped call (the kernels' bound)
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
@@ -656,13 +659,23 @@ q8_status q8_linear_grouped(const void* x, q8_dtype x_dtype, int64_t M, int64_t 
   return launched(q8::launch_gemm_group(xq, xs, gs, M, K, wq, w_scale, w_zp, group, N, bias, y, y_dtype, st));
 }
 
-q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                       int64_t v_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                       const float* cos, const float* sin, int64_t positions, int64_t rot_dim, int interleaved,
-                       const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int64_t S,
-                       int64_t max_pages, int64_t max_q, uint8_t* k_cache, uint8_t* k_exp, uint8_t* v_cache,
-                       uint8_t* v_exp, int64_t num_pages, int64_t page, void* q_out, void* stream) {
+namespace {
+
+// The arguments that q8_kv_append and q8_kv_append_norm share, checked, and what the kernels take.
+struct Norms {
+  const void *q_weight, *k_weight;
+  q8_dtype w_dtype;
+  float eps;
+  const int32_t* positions;      // of the tokens, or null
+};
+q8_status append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                 q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, const Norms* norms, const float* cos,
+                 const float* sin, int64_t positions, int64_t rot_dim, int interleaved, const int32_t* q_start,
+                 const int32_t* kv_len, const int32_t* block_table, int64_t S, int64_t max_pages, int64_t max_q,
+                 uint8_t* k_cache, uint8_t* k_exp, uint8_t* v_cache, uint8_t* v_exp, int64_t num_pages, int64_t page,
+                 void* q_out, void* stream) {
   if (!valid_dtype(dtype)) return Q8_ERR_BAD_DTYPE;
+  if (norms && (norms->q_weight || norms->k_weight) && !valid_dtype(norms->w_dtype)) return Q8_ERR_BAD_DTYPE;
   Q8_TRY(check_kv(T, Hkv, D, S, max_pages, max_q, num_pages, page));
   if (!q_start || !kv_len || !block_table || !k_cache || !k_exp || !v_cache || !v_exp || (T > 0 && (!k || !v)))
     return Q8_ERR_NULL_PTR;
@@ -677,12 +690,16 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
   auto bad_stride = [&](int64_t st, int64_t H) { return st < H * D || st % unit != 0; };
   if (T > 1 && (bad_stride(k_stride, Hkv) || bad_stride(v_stride, Hkv) || (has_q && bad_stride(q_stride, Hq))))
     return Q8_ERR_BAD_SHAPE;
+  if (norms && (norms->q_weight || norms->k_weight) && !(norms->eps > 0.0f && std::isfinite(norms->eps))) return Q8_ERR_BAD_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos) || !aligned16(sin) || !aligned16(k_cache) ||
-      !aligned16(v_cache) || !aligned16(q_out) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table))
+      !aligned16(v_cache) || !aligned16(q_out) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) ||
+      (norms && (!aligned16(norms->q_weight) || !aligned16(norms->k_weight) || !aligned4(norms->positions))))
     return Q8_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   Q8_TRY(check_device(st));
-  Q8_TRY(check_ptrs(st, {q, k, v, cos, sin, q_start, kv_len, block_table, k_cache, k_exp, v_cache, v_exp, q_out}));
+  Q8_TRY(check_ptrs(st, {q, k, v, cos, sin, q_start, kv_len, block_table, k_cache, k_exp, v_cache, v_exp, q_out,
+                         norms ? norms->q_weight : nullptr, norms ? norms->k_weight : nullptr,
+                         norms ? norms->positions : nullptr}));
   if (T == 0) return Q8_OK;
   q8::AppendArgs a{};
   a.kv = kv_view(k_cache, k_exp, v_cache, v_exp, q_start, kv_len, block_table, T, Hkv, S, max_pages, num_pages, page);
@@ -701,7 +718,40 @@ q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
   a.interleaved = interleaved != 0;
   const int64_t mq = bound_of(max_q, T);
   a.max_q = (int)mq;
-  return launched(q8::launch_kv_append(a, dtype, (int)D, st));
+  if (!norms) return launched(q8::launch_kv_append(a, dtype, (int)D, st));
+  a.qw = norms->q_weight;
+  a.kw = norms->k_weight;
+  a.w_dt = norms->w_dtype;
+  a.eps = norms->eps;
+  a.pos = norms->positions;
+  return launched(q8::launch_kv_append_norm(a, dtype, (int)D, st));
+}
+
+}  // namespace
+
+q8_status q8_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       const float* cos, const float* sin, int64_t positions, int64_t rot_dim, int interleaved,
+                       const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int64_t S,
+                       int64_t max_pages, int64_t max_q, uint8_t* k_cache, uint8_t* k_exp, uint8_t* v_cache,
+                       uint8_t* v_exp, int64_t num_pages, int64_t page, void* q_out, void* stream) {
+  return append(q, q_stride, k, k_stride, v, v_stride, dtype, T, Hq, Hkv, D, nullptr, cos, sin, positions, rot_dim,
+                interleaved, q_start, kv_len, block_table, S, max_pages, max_q, k_cache, k_exp, v_cache, v_exp, num_pages,
+                page, q_out, stream);
+}
+
+q8_status q8_kv_append_norm(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            const void* q_weight, const void* k_weight, q8_dtype w_dtype, float eps, const float* cos,
+                            const float* sin, int64_t positions, int64_t rot_dim, int interleaved,
+                            const int32_t* token_positions, const int32_t* q_start, const int32_t* kv_len,
+                            const int32_t* block_table, int64_t S, int64_t max_pages, int64_t max_q, uint8_t* k_cache,
+                            uint8_t* k_exp, uint8_t* v_cache, uint8_t* v_exp, int64_t num_pages, int64_t page,
+                            void* q_out, void* stream) {
+  const Norms norms{q_weight, k_weight, w_dtype, eps, token_positions};
+  return append(q, q_stride, k, k_stride, v, v_stride, dtype, T, Hq, Hkv, D, &norms, cos, sin, positions, rot_dim,
+                interleaved, q_start, kv_len, block_table, S, max_pages, max_q, k_cache, k_exp, v_cache, v_exp, num_pages,
+                page, q_out, stream);
 }
 
 size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q,
@@ -713,30 +763,42 @@ size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t 
   return attn_ws(T, Hq, Hkv, D, S, bound_of(max_q, T), bound_of(max_kv, kMaxRows), window).total;
 }
 
-q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv,
-                           int64_t D, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
-                           int64_t S, int64_t max_pages, int64_t max_q, int64_t max_kv, const uint8_t* k_cache,
-                           const uint8_t* k_exp, const uint8_t* v_cache, const uint8_t* v_exp, int64_t num_pages,
-                           int64_t page, float scale, int causal, int64_t window, void* out, float* lse,
-                           void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+// The tree of drafted tokens that the new ones are; null: a sequence.
+struct Tree {
+  const uint64_t* mask;
+  int64_t words;
+  const int32_t* positions;
+};
+q8_status attention(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                    const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int64_t S,
+                    int64_t max_pages, int64_t max_q, int64_t max_kv, const uint8_t* k_cache, const uint8_t* k_exp,
+                    const uint8_t* v_cache, const uint8_t* v_exp, int64_t num_pages, int64_t page, const Tree* tree,
+                    float scale, int causal, int64_t window, void* out, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   if (dtype != Q8_F16 && dtype != Q8_BF16) return Q8_ERR_BAD_DTYPE;
   Q8_TRY(check_kv(T, Hkv, D, S, max_pages, max_q, num_pages, page));
   if (!valid_heads(T, Hq, Hkv) || max_kv < 0 || max_kv > kMaxRows) return Q8_ERR_BAD_SHAPE;
+  if (tree && (tree->words < 1 || tree->words > kMaxMaskWords)) return Q8_ERR_BAD_SHAPE;
   if (T > 1 && (q_stride < Hq * D || q_stride % 8 != 0)) return Q8_ERR_BAD_SHAPE;
   if (!q_start || !kv_len || !block_table || !k_cache || !k_exp || !v_cache || !v_exp || (T > 0 && (!q || !out)))
     return Q8_ERR_NULL_PTR;
+  if (tree && T > 0 && !tree->mask) return Q8_ERR_NULL_PTR;
   if (!std::isfinite(scale) || window < 0) return Q8_ERR_BAD_ARG;
   window = window > kMaxTokens ? 0 : window;           // wider than any sequence: no window
   const int64_t mq = bound_of(max_q, T), mkv = bound_of(max_kv, kMaxRows);
   const AttnWs ws = attn_ws(T, Hq, Hkv, D, S, mq, mkv, window);
   if (ws.total > 0 && (!workspace || workspace_bytes < ws.total)) return Q8_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || (lse && !aligned4(lse)) ||
-      (ws.total > 0 && !aligned16(workspace)) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table))
+      (ws.total > 0 && !aligned16(workspace)) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) ||
+      (tree && ((reinterpret_cast<uintptr_t>(tree->mask) & 7) != 0 || !aligned4(tree->positions))))
     return Q8_ERR_ALIGN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   Q8_TRY(check_device(st));
   Q8_TRY(check_ptrs(st, {q, q_start, kv_len, block_table, k_cache, k_exp, v_cache, v_exp, out, lse,
-                         ws.total > 0 ? workspace : nullptr}));
+                         ws.total > 0 ? workspace : nullptr, tree ? tree->mask : nullptr,
+                         tree ? tree->positions : nullptr}));
   if (T == 0) return Q8_OK;
   q8::AttnArgs a{};
   a.kv = kv_view(k_cache, k_exp, v_cache, v_exp, q_start, kv_len, block_table, T, Hkv, S, max_pages, num_pages, page);
@@ -754,7 +816,183 @@ q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int6
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part);
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.ml);
   }
-  return launched(q8::launch_attention(a, dtype, (int)D, st));
+  if (!tree) return launched(q8::launch_attention(a, dtype, (int)D, st));
+  a.mask = tree->mask;
+  a.words = (int)tree->words;
+  a.pos = tree->positions;
+  return launched(q8::launch_attention_tree(a, dtype, (int)D, st));
+}
+
+}  // namespace
+
+q8_status q8_attention_kv8(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv,
+                           int64_t D, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                           int64_t S, int64_t max_pages, int64_t max_q, int64_t max_kv, const uint8_t* k_cache,
+                           const uint8_t* k_exp, const uint8_t* v_cache, const uint8_t* v_exp, int64_t num_pages,
+                           int64_t page, float scale, int causal, int64_t window, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  return attention(q, q_stride, dtype, T, Hq, Hkv, D, q_start, kv_len, block_table, S, max_pages, max_q, max_kv, k_cache,
+                   k_exp, v_cache, v_exp, num_pages, page, nullptr, scale, causal, window, out, lse, workspace,
+                   workspace_bytes, stream);
+}
+
+q8_status q8_attention_kv8_tree(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv,
+                                int64_t D, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                int64_t S, int64_t max_pages, int64_t max_q, int64_t max_kv, const uint8_t* k_cache,
+                                const uint8_t* k_exp, const uint8_t* v_cache, const uint8_t* v_exp, int64_t num_pages,
+                                int64_t page, const uint64_t* mask, int64_t mask_words, const int32_t* token_positions,
+                                float scale, int64_t window, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const Tree tree{mask, mask_words, token_positions};
+  return attention(q, q_stride, dtype, T, Hq, Hkv, D, q_start, kv_len, block_table, S, max_pages, max_q, max_kv, k_cache,
+                   k_exp, v_cache, v_exp, num_pages, page, &tree, scale, 0, window, out, lse, workspace, workspace_bytes,
+                   stream);
+}
+
+namespace {
+
+// The caches of all layers: every pointer given and aligned, no layer twice.
+q8_status check_layers(uint8_t* const* k, uint8_t* const* ke, uint8_t* const* v, uint8_t* const* ve, int64_t layers) {
+  if (layers < 1 || layers > kMaxLayers) return Q8_ERR_BAD_SHAPE;
+  if (!k || !ke || !v || !ve) return Q8_ERR_NULL_PTR;
+  uintptr_t seen[kMaxLayers];
+  for (int64_t i = 0; i < layers; ++i) {
+    if (!k[i] || !ke[i] || !v[i] || !ve[i]) return Q8_ERR_NULL_PTR;
+    if (!aligned16(k[i]) || !aligned16(v[i])) return Q8_ERR_ALIGN;
+    seen[i] = reinterpret_cast<uintptr_t>(k[i]);
+  }
+  std::sort(seen, seen + layers);
+  return std::adjacent_find(seen, seen + layers) == seen + layers ? Q8_OK : Q8_ERR_BAD_ARG;
+}
+q8_status check_layer_ptrs(hipStream_t st, uint8_t* const* k, uint8_t* const* ke, uint8_t* const* v, uint8_t* const* ve,
+                           int64_t layers) {
+  for (int64_t i = 0; i < layers; ++i) Q8_TRY(check_ptrs(st, {k[i], ke[i], v[i], ve[i]}));
+  return Q8_OK;
+}
+void take_layers(q8::CacheLayer* to, uint8_t* const* k, uint8_t* const* ke, uint8_t* const* v, uint8_t* const* ve,
+                 int64_t from, int n) {
+  for (int i = 0; i < n; ++i) to[i] = q8::CacheLayer{k[from + i], v[from + i], ke[from + i], ve[from + i]};
+}
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {       // of int32 arrays
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * (uint64_t)nb && y < x + 4 * (uint64_t)na;
+}
+
+struct ForkWs { size_t first, fresh, taken, copies, total; };
+ForkWs fork_ws(int64_t S, int64_t S_out, int64_t num_pages) {
+  Carve c;
+  ForkWs w;
+  w.first = c.take((size_t)S * 4);
+  w.fresh = c.take((size_t)S_out * 4);
+  w.taken = c.take((size_t)num_pages * 4);
+  w.copies = c.take((size_t)S_out * 8);
+  w.total = c.off;
+  return w;
+}
+
+}  // namespace
+
+q8_status q8_kv_compact(uint8_t* const* k_cache, uint8_t* const* k_exp, uint8_t* const* v_cache, uint8_t* const* v_exp,
+                        int64_t layers, int64_t Hkv, int64_t D, const int32_t* q_start, const int32_t* kv_len,
+                        const int32_t* block_table, int64_t S, int64_t max_pages, int64_t num_pages, int64_t page,
+                        const int32_t* keep, int64_t max_keep, const int32_t* n_keep, int32_t* len_out, void* stream) {
+  Q8_TRY(check_kv(0, Hkv, D, S, max_pages, 0, num_pages, page));
+  if (max_keep < 0 || max_keep > kMaxTokens) return Q8_ERR_BAD_SHAPE;
+  if (!q_start || !kv_len || !block_table || (max_keep > 0 && !keep) || !n_keep || !len_out) return Q8_ERR_NULL_PTR;
+  Q8_TRY(check_layers(k_cache, k_exp, v_cache, v_exp, layers));
+  if (!aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) || !aligned4(keep) || !aligned4(n_keep) ||
+      !aligned4(len_out))
+    return Q8_ERR_ALIGN;
+  // every workgroup reads these while one of them writes the lengths
+  if (overlap(len_out, S, kv_len, S) || overlap(len_out, S, q_start, S + 1) || overlap(len_out, S, n_keep, S) ||
+      overlap(len_out, S, block_table, S * max_pages) || (keep && overlap(len_out, S, keep, S * max_keep)))
+    return Q8_ERR_BAD_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {q_start, kv_len, block_table, keep, n_keep, len_out}));
+  if (debug_validate()) Q8_TRY(check_layer_ptrs(st, k_cache, k_exp, v_cache, v_exp, layers));
+  q8::CompactArgs a{};
+  a.kv = kv_view(nullptr, nullptr, nullptr, nullptr, q_start, kv_len, block_table, 0, Hkv, S, max_pages, num_pages, page);
+  a.keep = keep;
+  a.n_keep = n_keep;
+  a.len_out = len_out;
+  a.width = (int)max_keep;
+  for (int64_t i = 0; i < layers; i += q8::kLayers) {
+    const int n = (int)(layers - i < q8::kLayers ? layers - i : q8::kLayers);
+    take_layers(a.layer, k_cache, k_exp, v_cache, v_exp, i, n);
+    Q8_TRY(launched(q8::launch_kv_compact(a, (int)D, n, st)));
+    a.len_out = nullptr;
+  }
+  return Q8_OK;
+}
+
+size_t q8_kv_fork_workspace_bytes(int64_t S, int64_t S_out, int64_t num_pages) {
+  if (S < 1 || S > 32768 || S_out < 1 || S_out > 32768 || num_pages < 1 || num_pages > kMaxRows) return 0;
+  return fork_ws(S, S_out, num_pages).total;
+}
+
+q8_status q8_kv_fork(uint8_t* const* k_cache, uint8_t* const* k_exp, uint8_t* const* v_cache, uint8_t* const* v_exp,
+                     int64_t layers, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page,
+                     const int32_t* block_table, const int32_t* kv_len, const int32_t* refs, int64_t S,
+                     int64_t max_pages, const int32_t* parent, int64_t S_out, int64_t room, int32_t* table_out,
+                     int32_t* len_out, int32_t* refs_out, int32_t* missing, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  Q8_TRY(check_kv(0, Hkv, D, S, max_pages, 0, num_pages, page));
+  if (S_out < 1 || S_out > 32768 || room < 0 || room > kMaxTokens || S_out * max_pages > kMaxRows) return Q8_ERR_BAD_SHAPE;
+  if (!block_table || !kv_len || !refs || !parent || !table_out || !len_out || !refs_out || !missing) return Q8_ERR_NULL_PTR;
+  Q8_TRY(check_layers(k_cache, k_exp, v_cache, v_exp, layers));
+  const ForkWs ws = fork_ws(S, S_out, num_pages);
+  if (!workspace || workspace_bytes < ws.total) return Q8_ERR_WORKSPACE;
+  if (!aligned4(block_table) || !aligned4(kv_len) || !aligned4(refs) || !aligned4(parent) || !aligned4(table_out) ||
+      !aligned4(len_out) || !aligned4(refs_out) || !aligned4(missing) || !aligned16(workspace))
+    return Q8_ERR_ALIGN;
+  // nothing is written over what is read, or twice
+  struct Array {
+    const void* p;
+    int64_t n;
+  };
+  const Array out[] = {{table_out, S_out * max_pages}, {len_out, S_out}, {refs_out, num_pages}, {missing, 1},
+                       {workspace, (int64_t)(ws.total / 4)}};
+  const Array in[] = {{block_table, S * max_pages}, {kv_len, S}, {refs, num_pages}, {parent, S_out}};
+  for (const Array& o : out) {
+    for (const Array& i : in)
+      if (overlap(o.p, o.n, i.p, i.n)) return Q8_ERR_BAD_ARG;
+    for (const Array& other : out)
+      if (&other != &o && overlap(o.p, o.n, other.p, other.n)) return Q8_ERR_BAD_ARG;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Q8_TRY(check_device(st));
+  Q8_TRY(check_ptrs(st, {block_table, kv_len, refs, parent, table_out, len_out, refs_out, missing, workspace}));
+  if (debug_validate()) Q8_TRY(check_layer_ptrs(st, k_cache, k_exp, v_cache, v_exp, layers));
+  char* const base = static_cast<char*>(workspace);
+  q8::ForkArgs a{};
+  a.table = block_table;
+  a.kv_len = kv_len;
+  a.refs = refs;
+  a.parent = parent;
+  a.table_out = table_out;
+  a.len_out = len_out;
+  a.refs_out = refs_out;
+  a.missing = missing;
+  a.first = reinterpret_cast<int32_t*>(base + ws.first);
+  a.fresh = reinterpret_cast<int32_t*>(base + ws.fresh);
+  a.taken = reinterpret_cast<int32_t*>(base + ws.taken);
+  a.copies = reinterpret_cast<int32_t*>(base + ws.copies);
+  a.room = room;
+  a.page_bytes = Hkv * page * D;
+  a.seqs = (int)S;
+  a.outs = (int)S_out;
+  a.max_pages = (int)max_pages;
+  a.num_pages = (int)num_pages;
+  a.page = (int)page;
+  a.kv_heads = (int)Hkv;
+  Q8_TRY(launched(q8::launch_kv_fork(a, st)));
+  for (int64_t i = 0; i < layers; i += q8::kLayers) {
+    const int n = (int)(layers - i < q8::kLayers ? layers - i : q8::kLayers);
+    take_layers(a.layer, k_cache, k_exp, v_cache, v_exp, i, n);
+    Q8_TRY(launched(q8::launch_copy_pages(a, n, st)));
+  }
+  return Q8_OK;
 }
 
 q8_status q8_quantize_weight_block(const void* w, q8_dtype w_dtype, int64_t N, int64_t K, uint8_t* wq, float* w_scale,

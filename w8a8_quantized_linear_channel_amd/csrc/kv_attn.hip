@@ -87,19 +87,42 @@ __device__ __forceinline__ int without_nan(int x, uint32_t mask) {
   const uint32_t t = (((uint32_t)x & 0x7f7f7f7fu) + 0x01010101u) & mask;
   return x & (int)~((t << 1) - (t >> 7));
 }
+// ------------------------------------------------------------ drafted trees
+// TREE: the new tokens continue each other as a tree.  A row sees the cached keys (those before `past`, in
+// its window) and the new tokens that its mask names, a bit each in words of 64.
+//
+// The bits of N keys from past + o on (cached ones set), from the mask words of a row.
+template <int N>
+__device__ __forceinline__ uint32_t drafted(const uint64_t* mask, int words, int o) {
+  constexpr uint32_t all = (uint32_t)(((uint64_t)1 << N) - 1);
+  if (o <= -N) return all;
+  if (o < 0) return (uint32_t)(mask[0] << -o | (((uint64_t)1 << -o) - 1)) & all;
+  const int i = o >> 6, sh = o & 63;
+  const uint64_t lo = i < words ? mask[i] : 0, hi = sh > 64 - N && i + 1 < words ? mask[i + 1] : 0;
+  return (uint32_t)(lo >> sh | hi << 1 << (63 - sh)) & all;
+}
+// The position of token `tok` (of n after `past` cached ones), by which its window reaches back.
+__device__ __forceinline__ int drafted_at(const AttnArgs& a, int first, int tok, int past, int n) {
+  int p = a.pos ? a.pos[first + tok] : past + tok;
+  p = p < past ? past : p;
+  return p < past + n ? p : past + n - 1;
+}
+
 // NaN into the output of row `row` at position pos (of this split, share [kb0, kb1) of its keys) for the
 // features d0 + step i + 0 .. 3 in which a key that it sees, outside [all_lo, all_hi), holds a NaN code.
-template <int D>
+template <int D, bool TREE>
 __device__ __forceinline__ void put_nan(const AttnArgs& a, int s, int head, int64_t row, int pos, int split, bool split_out,
-                                        int kb0, int kb1, int all_lo, int all_hi, int d0, int step) {
+                                        int kb0, int kb1, int all_lo, int all_hi, int d0, int step, int past) {
   const KvView kv = a.kv;
-  int low = a.window > 0 ? pos - a.window + 1 : 0, high = a.causal && pos + 1 < kb1 ? pos + 1 : kb1;
+  int low = a.window > 0 ? pos - a.window + 1 : 0, high = !TREE && a.causal && pos + 1 < kb1 ? pos + 1 : kb1;
+  if (TREE && low > past) low = past;
   low = low > kb0 ? low : kb0;
   for (int key = low; key < high; ++key) {
     if (key >= all_lo && key < all_hi) {
       key = all_hi - 1;
       continue;
     }
+    if (TREE && key >= past && !(drafted<16>(a.mask + row / a.heads * a.words, a.words, key - past) & 1)) continue;
     int p = kv.table[(int64_t)s * kv.max_pages + (key >> (31 - __builtin_clz(kv.page)))];
     p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
     const uint8_t* const v = kv.v + ((int64_t)p * kv.kv_heads + head) * D * kv.page + (key & (kv.page - 1));
@@ -135,7 +158,30 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int s) {
   return r;
 }
 
-template <int D, int DT, int NW>
+// The keys that some of a block's rows see, [lo, hi), and those that all of them do (within these); pos0,
+// pos1: the slots of its first and last token.
+struct Keys {
+  int lo, hi, all_lo, all_hi;
+};
+template <bool TREE>
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, const Span& sp, int pos0, int pos1) {
+  Keys k;
+  if constexpr (TREE) {
+    // positions lie from past to past + n - 1
+    k.hi = sp.total;
+    k.all_hi = sp.past < sp.total ? sp.past : sp.total;
+    k.lo = a.window > 0 && sp.past - a.window + 1 > 0 ? sp.past - a.window + 1 : 0;
+    k.all_lo = a.window > 0 && sp.past + sp.n - a.window > 0 ? sp.past + sp.n - a.window : 0;
+  } else {
+    k.hi = a.causal ? (pos1 + 1 < sp.total ? pos1 + 1 : sp.total) : sp.total;
+    k.all_hi = a.causal ? (pos0 + 1 < sp.total ? pos0 + 1 : sp.total) : sp.total;
+    k.lo = a.window > 0 && pos0 - a.window + 1 > 0 ? pos0 - a.window + 1 : 0;
+    k.all_lo = a.window > 0 && pos1 - a.window + 1 > 0 ? pos1 - a.window + 1 : 0;
+  }
+  return k;
+}
+
+template <int D, int DT, int NW, bool TREE>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const AttnArgs a, int row_tiles, int chunk) {
   constexpr int KS = D / 32;        // MFMA steps over the features
   constexpr int KL = D / 64;        // 16-byte loads of a lane's share of a key
@@ -163,9 +209,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
     // this lane's row and the keys that it sees: [low, high)
     const int row = r0 + lr, rc = row < rows ? row : rows - 1;
     const int tok = rc / group, hq = rc - tok * group;
-    const int pos = sp.past + tok;
-    int high = a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total;
-    const int low = a.window > 0 ? pos - a.window + 1 : 0;
+    const int pos = TREE ? drafted_at(a, sp.first, tok, sp.past, sp.n) : sp.past + tok;
+    int high = !TREE && a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total;
+    int low = a.window > 0 ? pos - a.window + 1 : 0;
+    if (TREE && low > sp.past) low = sp.past;        // (the window is the cached keys' alone)
     if (row >= rows) high = 0;
     // features 64 i + 16 g .. + 15 of the row, as the lane's loads of a key give them
     v4i qf[KS];
@@ -178,11 +225,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
     // keys that any row of the tile sees
     const int last = (r0 + 16 < rows ? r0 + 16 : rows) - 1;
     const int pos0 = sp.past + r0 / group, pos1 = sp.past + last / group;
-    const int klo = a.window > 0 && pos0 - a.window + 1 > 0 ? pos0 - a.window + 1 : 0;
-    const int khi = a.causal ? (pos1 + 1 < sp.total ? pos1 + 1 : sp.total) : sp.total;
-    // those that all of them see, and whether there are others
-    const int all_lo = a.window > 0 && pos1 - a.window + 1 > 0 ? pos1 - a.window + 1 : 0;
-    const int all_hi = a.causal ? (pos0 + 1 < sp.total ? pos0 + 1 : sp.total) : sp.total;
+    const Keys ks = keys_of<TREE>(a, sp, pos0, pos1);
+    const int klo = ks.lo, khi = ks.hi, all_lo = ks.all_lo, all_hi = ks.all_hi;
     const bool mixed = all_lo != klo || all_hi != khi;
     // this workgroup's share: `chunk` keys from a multiple of kTile on, the last share all that is left
     const int base = klo & ~(kTile - 1);
@@ -247,14 +291,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
       }
       // the scores; register 4 t + i is key keyv + 4 t + i
       const float kscale = exp_byte(kb8) * a.scale_log2;
-      const bool edge = kb < klo || kb + kTile > khi, all = kb >= low && kb + kTile <= high;
+      const bool edge = kb < klo || kb + kTile > khi;
+      const bool all = kb >= low && kb + kTile <= high && (!TREE || kb + kTile <= sp.past);
+      uint32_t bits = 0xffffu;
+      if constexpr (TREE)
+        if (kb + kTile > sp.past) bits = drafted<16>(a.mask + (int64_t)(sp.first + tok) * a.words, a.words, keyv - sp.past);
       float mx = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = keyv + 4 * t + i;
-          const float x = all || (key >= low && key < high) ? sc[t][i] * kscale : -INFINITY;
+          const float x = all || (key >= low && key < high && (!TREE || (bits >> (4 * t + i) & 1))) ? sc[t][i] * kscale : -INFINITY;
           sc[t][i] = x;
           mx = fmaxf(mx, x);
         }
@@ -416,7 +464,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_rows(const A
           *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
         }
       }
-      if (__builtin_expect(careful, 0)) put_nan<D>(a, s, head, orow, sp.past + otok, split, split_out, kb0, kb1, all_lo, all_hi, part * 4, 64);
+      if (__builtin_expect(careful, 0)) put_nan<D, TREE>(a, s, head, orow, TREE ? drafted_at(a, sp.first, otok, sp.past, sp.n) : sp.past + otok, split, split_out, kb0, kb1, all_lo, all_hi, part * 4, 64, sp.past);
       if (part == 0) {
         if (split_out) {
           float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
@@ -484,7 +532,7 @@ template <int D>
 __device__ __forceinline__ constexpr int key_swz(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
 __device__ __forceinline__ int val_swz(int d) { return (d >> 1) & 7; }
 
-template <int D, int DT, int NW>
+template <int D, int DT, int NW, bool TREE>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const AttnArgs a, int row_tiles, int splits,
                                                                          int chunk) {
   constexpr int kThr = 64 * NW, kRows = 32 * NW;
@@ -526,7 +574,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     // this lane's row (rows past the end repeat the last one and are not stored)
     const int row = r0 + 32 * wave + lr, rc = row < rows ? row : rows - 1;
     const int tok = rc / group, hq = rc - tok * group;
-    const int pos = sp.past + tok;
     v4i qf[KS];
     {
       int qh = lh;
@@ -543,16 +590,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     // keys that any row of the block sees, and those that every row of the wave does
     const int last = (r0 + kRows < rows ? r0 + kRows : rows) - 1;
     const int p0 = sp.past + r0 / group, p1 = sp.past + last / group;
-    const int klo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
-    const int khi = a.causal ? (p1 + 1 < sp.total ? p1 + 1 : sp.total) : sp.total;
+    const Keys ks = keys_of<TREE>(a, sp, p0, p1);
+    const int klo = ks.lo, khi = ks.hi, block_lo = ks.all_lo, block_hi = ks.all_hi;
     const int w0 = r0 + 32 * wave < rows ? r0 + 32 * wave : rows - 1;
     const int w1 = w0 + 31 < rows ? w0 + 31 : rows - 1;
     const int pw0 = sp.past + w0 / group, pw1 = sp.past + w1 / group;
-    const int all_hi = a.causal ? (pw0 + 1 < sp.total ? pw0 + 1 : sp.total) : sp.total;
-    const int all_lo = a.window > 0 ? pw1 - a.window + 1 : 0;
-    // those that every row of the block does, and whether there are others
-    const int block_hi = a.causal ? (p0 + 1 < sp.total ? p0 + 1 : sp.total) : sp.total;
-    const int block_lo = a.window > 0 && p1 - a.window + 1 > 0 ? p1 - a.window + 1 : 0;
+    const Keys kw = keys_of<TREE>(a, sp, pw0, pw1);
+    const int all_lo = kw.all_lo, all_hi = kw.all_hi;
+    // whether some row of the block does not see a key that another one does
     const bool mixed = block_lo != klo || block_hi != khi;
     const int base = klo & ~(kStep - 1);
     const int64_t from = (int64_t)split * chunk;
@@ -690,12 +735,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
     auto settle = [&](int exps, int kb, float mx, bool again) {
       if (!(kb >= all_lo && kb + kStep <= all_hi)) {
         // register 16 t + r is key kb + 32 h + 16 t + r: the row sees those from `low` to below `high`
-        const int high = (a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total) - kb - 32 * lh;
-        const int low = (a.window > 0 ? pos - a.window + 1 : 0) - kb - 32 * lh;
+        const int pos = TREE ? drafted_at(a, sp.first, tok, sp.past, sp.n) : sp.past + tok;
+        const int high = (!TREE && a.causal ? (pos + 1 < sp.total ? pos + 1 : sp.total) : sp.total) - kb - 32 * lh;
+        int low = (a.window > 0 ? pos - a.window + 1 : 0) - kb - 32 * lh;
+        uint32_t bits = ~0u;
+        if constexpr (TREE) {
+          const int o = kb + 32 * lh - sp.past;
+          low = low < -o ? low : -o;                  // (the window is the cached keys' alone)
+          bits = drafted<32>(a.mask + (int64_t)(sp.first + tok) * a.words, a.words, o);
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sn[t][r] = 16 * t + r >= low && 16 * t + r < high ? sn[t][r] : -INFINITY;
+          for (int r = 0; r < 16; ++r)
+            sn[t][r] = 16 * t + r >= low && 16 * t + r < high && (!TREE || (bits >> (16 * t + r) & 1)) ? sn[t][r] : -INFINITY;
         mx = highest();
       }
       // not 0: a masked score of -inf stays one
@@ -866,7 +919,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
           if (splits > 1) *(v4f*)(a.part + ((int64_t)split * kv.tokens * a.heads + orow) * D + d) = o;
           else *(v2i*)((uint16_t*)a.out + orow * D + d) = v2i{(int)pack2_out<DT>(o[0], o[1]), (int)pack2_out<DT>(o[2], o[3])};
         }
-      if (__builtin_expect(careful, 0)) put_nan<D>(a, s, head, orow, sp.past + otok, split, splits > 1, kb0, kb1, block_lo, block_hi, 4 * oh, 8);
+      if (__builtin_expect(careful, 0)) put_nan<D, TREE>(a, s, head, orow, TREE ? drafted_at(a, sp.first, otok, sp.past, sp.n) : sp.past + otok, split, splits > 1, kb0, kb1, block_lo, block_hi, 4 * oh, 8, sp.past);
       if (oh == 0) {
         if (splits > 1) {
           float* ml = a.part_ml + ((int64_t)split * kv.tokens * a.heads + orow) * 2;
@@ -935,7 +988,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int blocks,
   }
 }
 
-template <int D, int DT>
+template <int D, int DT, bool TREE>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.heads / a.kv.kv_heads);
   const AttnPlan p = attn_plan(rows, D, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
@@ -945,16 +998,16 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
     // 8 waves (half as many tiles one after the other: 513 keys, 8 kv heads, 11.0 against 9.2 us) where
     // every workgroup has a CU to itself
     if (D < 256 && (int64_t)grid.x * grid.y * grid.z <= 256) {
-      if constexpr (D < 256) k_attn_rows<D, DT, 8><<<grid, 512, 0, st>>>(a, blocks, p.chunk);
+      if constexpr (D < 256) k_attn_rows<D, DT, 8, TREE><<<grid, 512, 0, st>>>(a, blocks, p.chunk);
     } else {
-      k_attn_rows<D, DT, 4><<<grid, 256, 0, st>>>(a, blocks, p.chunk);
+      k_attn_rows<D, DT, 4, TREE><<<grid, 256, 0, st>>>(a, blocks, p.chunk);
     }
   } else {
     const unsigned grid = (unsigned)(p.blocks * a.kv.seqs * a.kv.kv_heads * p.splits);
     if constexpr (D != 128)
-      if (p.per == 128) k_attn_tiles<D, DT, 4><<<grid, 256, 0, st>>>(a, blocks, p.splits, p.chunk);
+      if (p.per == 128) k_attn_tiles<D, DT, 4, TREE><<<grid, 256, 0, st>>>(a, blocks, p.splits, p.chunk);
     if constexpr (D != 256)
-      if (p.per == 256) k_attn_tiles<D, DT, 8><<<grid, 512, 0, st>>>(a, blocks, p.splits, p.chunk);
+      if (p.per == 256) k_attn_tiles<D, DT, 8, TREE><<<grid, 512, 0, st>>>(a, blocks, p.splits, p.chunk);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -962,12 +1015,12 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   k_attn_join<D, DT><<<(unsigned)(jb * a.kv.seqs), 256, 0, st>>>(a, (int)jb, p.splits);
   return hipGetLastError();
 }
-template <int DT>
+template <int DT, bool TREE>
 hipError_t launch_dt(const AttnArgs& a, int dim, hipStream_t st) {
   switch (dim) {
-    case 64: return launch_dim<64, DT>(a, st);
-    case 128: return launch_dim<128, DT>(a, st);
-    default: return launch_dim<256, DT>(a, st);
+    case 64: return launch_dim<64, DT, TREE>(a, st);
+    case 128: return launch_dim<128, DT, TREE>(a, st);
+    default: return launch_dim<256, DT, TREE>(a, st);
   }
 }
 
@@ -978,7 +1031,10 @@ int attn_splits(int heads, int kv_heads, int dim, int seqs, int64_t max_q, int64
 }
 
 hipError_t launch_attention(const AttnArgs& a, int dt, int dim, hipStream_t st) {
-  return dt == DT_F16 ? launch_dt<DT_F16>(a, dim, st) : launch_dt<DT_BF16>(a, dim, st);
+  return dt == DT_F16 ? launch_dt<DT_F16, false>(a, dim, st) : launch_dt<DT_BF16, false>(a, dim, st);
+}
+hipError_t launch_attention_tree(const AttnArgs& a, int dt, int dim, hipStream_t st) {
+  return dt == DT_F16 ? launch_dt<DT_F16, true>(a, dim, st) : launch_dt<DT_BF16, true>(a, dim, st);
 }
 
 }  // namespace q8

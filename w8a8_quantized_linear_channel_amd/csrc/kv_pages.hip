@@ -1,0 +1,421 @@
+// Pages of the 8-bit key/value cache moved in every layer at once: kept drafts
+// to the front of their slots (compact), sequences continued by others (fork).
+//
+// Compact.  One wave per (sequence, kv head, K or V, layer) goes through the
+// pages that receive tokens in order.  A kept token's slot is at or behind the
+// place that it goes to, and a wave reads a group of tokens before it writes
+// them, so nothing is overwritten before it is read.  A page's scale follows the
+// append's rule, in whole numbers: code c of a page with exponent byte b asks for
+// the byte b + k(c), k the least whole number with |e4m3(c)| <= 448 2^k.
+//
+// Fork.  One workgroup decides everything about the tables: which entries of a
+// row are shared, kept or new, the counts, and the lowest free pages for the new
+// ones, numbered by row and entry; then any number of workgroups copy pages.
+#include "q8_device.hpp"
+#include "q8_kv.hpp"
+
+namespace q8 {
+namespace {
+
+// The least k with |e4m3(c)| <= 448 2^k, c a code's 7 magnitude bits (1 .. 126)
+__device__ __forceinline__ int code_scale(int c) {
+  // 448 = 1.75 2^8: a normal code 2^(x - 7) (1 + m / 8) asks for x - 15, one more where m is 7; a subnormal
+  // one, m 2^-9 = 2^(h - 9) (1 + f), f at most 0.75, for h - 17
+  const int x = c >> 3, m = c & 7;
+  return x > 0 ? x - 15 + (m == 7 ? 1 : 0) : 14 - __builtin_clz(m);
+}
+// The exponent byte that a code of a page with byte b asks for; 0 for zeros and NaN codes
+__device__ __forceinline__ int wanted(int c, int b) {
+  c &= 0x7f;
+  if (c == 0 || c == 0x7f) return 0;
+  const int w = b + code_scale(c);
+  return w < 0 ? 0 : w;
+}
+// The largest magnitude among four codes, NaN codes aside (as they order)
+__device__ __forceinline__ int largest4(uint32_t w, int most) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = (int)(w >> (8 * i)) & 0x7f;
+    most = c != 0x7f && c > most ? c : most;
+  }
+  return most;
+}
+// Four codes times 2^shift, NaN codes as they are
+__device__ __forceinline__ uint32_t rescaled4(uint32_t w, int shift) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  const uint32_t t = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u, nan = (t << 1) - (t >> 7);
+  return (pack4_e4m3(__builtin_ldexpf(lo[0], shift), __builtin_ldexpf(lo[1], shift), __builtin_ldexpf(hi[0], shift),
+                     __builtin_ldexpf(hi[1], shift)) & ~nan) | (w & nan);
+}
+__device__ __forceinline__ int wave_max_i(int v) {
+  v = dpp_row_reduce(v, [](int a, int b) { return a > b ? a : b; });
+  const int a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+  const int c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+  const int x = a > b ? a : b, y = c > d ? c : d;
+  return x > y ? x : y;
+}
+
+// The kept path of a sequence as far as it is one: entries i, keep[i] from i on, growing, below n.  Returns
+// their number; `stay` receives how many are in place at its front.
+__device__ __forceinline__ int path_of(const int32_t* keep, int most, int n, int lane, int* stay) {
+  int total = 0, still = 0;
+  for (int base = 0;; base += 64) {
+    const int i = base + lane;
+    const bool in = i < most;
+    const int k = in ? keep[i] : -1, before = in && i > 0 ? keep[i - 1] : -1;
+    const uint64_t ok = __ballot(in && k >= i && k < n && k > before), same = __ballot(in && k == i);
+    const int run = ok == ~0ull ? 64 : __builtin_ctzll(~ok);
+    const uint64_t mine = run == 64 ? ~0ull : ((uint64_t)1 << run) - 1, off = mine & ~same;
+    if (still == base) still += off ? __builtin_ctzll(off) : run;
+    total += run;
+    if (run < 64) break;
+  }
+  *stay = still;
+  return total;
+}
+
+template <int D>
+__device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int s, int head, bool is_v, int lane, bool says) {
+  const KvView& kv = a.kv;
+  const int page_log2 = 31 - __builtin_clz(kv.page), page = kv.page;
+  int end = kv.q_start[s + 1], first = kv.q_start[s];
+  end = end < 0 ? 0 : end;
+  first = first < 0 ? 0 : (first > end ? end : first);
+  const int n = end - first, len = kv.kv_len[s] < 0 ? 0 : kv.kv_len[s], past = len - n;
+  int most = a.n_keep[s];
+  most = most < 0 ? 0 : (most > a.width ? a.width : most);
+  const int32_t* const keep = a.keep + (int64_t)s * a.width;
+  int stay;
+  const int kept = path_of(keep, most, n, lane, &stay);
+  if (says && lane == 0) a.len_out[s] = past + kept < 0 ? 0 : past + kept;
+  const int64_t cap = (int64_t)kv.max_pages * page;
+  // the slots that receive a token
+  int lo = past + stay < 0 ? 0 : past + stay;
+  const int hi = past + kept < cap ? past + kept : (int)cap;
+  uint8_t* const codes = is_v ? layer.v : layer.k;
+  uint8_t* const exps = is_v ? layer.ve : layer.ke;
+  const int32_t* const table = kv.table + (int64_t)s * kv.max_pages;
+  auto page_at = [&](int slot) {
+    if (slot < 0 || slot >= cap) return -1;
+    const int p = table[slot >> page_log2];
+    return p < kv.num_pages ? p : -1;
+  };
+  for (; lo < hi; lo = (lo & ~(page - 1)) + page) {
+    const int stop = (lo & ~(page - 1)) + page, top = hi < stop ? hi : stop;
+    const int to = page_at(lo);
+    if (to < 0) continue;
+    const int64_t th = (int64_t)to * kv.kv_heads + head;
+    uint8_t* const dst = codes + th * page * D;
+    const int had = exps[th];
+    const bool fresh = (lo & (page - 1)) == 0;
+    // a token's source: offset of its head's codes, place in the page and exponent byte; -1 without one
+    struct Source {
+      int64_t at;
+      int off, b;
+    };
+    auto source = [&](int slot) {
+      Source r{-1, 0, 0};
+      const int from = past + keep[slot - past], p = page_at(from);
+      if (p < 0) return r;
+      const int64_t ph = (int64_t)p * kv.kv_heads + head;
+      r.at = ph * page * D;
+      r.off = from & (page - 1);
+      r.b = exps[ph];
+      return r;
+    };
+    int want = -1;
+    auto settle = [&]() {            // the page's new byte, -1 where nothing comes
+      want = wave_max_i(want);
+      return want < 0 ? -1 : (fresh || want > had ? want : had);
+    };
+    if (!is_v) {
+      constexpr int C = D / 16, G = 64 / C;         // chunks of a token, tokens at once
+      const int c = lane % C;
+      auto load = [&](int slot, Source& r, v4i& x) {
+        r = source(slot);
+        x = r.at >= 0 ? *(const v4i*)(codes + r.at + r.off * D + 16 * c) : v4i{0, 0, 0, 0};
+      };
+      Source r0{-1, 0, 0};
+      v4i x0 = {0, 0, 0, 0};
+      for (int slot = lo + lane / C; slot < top; slot += G) {
+        Source r;
+        v4i x;
+        load(slot, r, x);
+        if (r.at < 0) continue;
+        int big = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) big = largest4((uint32_t)x[w], big);
+        const int w = wanted(big, r.b);
+        want = w > want ? w : want;
+        if (slot < lo + G) {
+          r0 = r;
+          x0 = x;
+        }
+      }
+      const int b = settle();
+      if (b < 0) continue;
+      if (!fresh && b != had)
+        for (int i = lane / C; i < (lo & (page - 1)); i += G) {
+          v4i* const p = (v4i*)(dst + i * D + 16 * c);
+          v4i x = *p;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) x[w] = (int)rescaled4((uint32_t)x[w], had - b);
+          *p = x;
+        }
+      for (int slot = lo + lane / C; slot < top; slot += G) {
+        Source r = r0;
+        v4i x = x0;
+        if (slot >= lo + G) load(slot, r, x);
+        if (r.at < 0) continue;
+        if (r.b != b)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) x[w] = (int)rescaled4((uint32_t)x[w], r.b - b);
+        *(v4i*)(dst + (slot & (page - 1)) * D + 16 * c) = x;
+      }
+      if (lane == 0 && b != had) exps[th] = (uint8_t)b;
+    } else {
+      constexpr int F = D / 64;                     // features of a lane
+      for (int slot = lo; slot < top; ++slot) {
+        const Source r = source(slot);
+        if (r.at < 0) continue;
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+          const int w = wanted(codes[r.at + (int64_t)(lane + 64 * j) * page + r.off], r.b);
+          want = w > want ? w : want;
+        }
+      }
+      const int b = settle();
+      if (b < 0) continue;
+      if (!fresh && b != had) {
+        const int old = lo & (page - 1);
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+          for (int i = 0; i < old; i += 4) {
+            uint32_t* const p = (uint32_t*)(dst + (lane + 64 * j) * page + i);
+            const uint32_t mask = old - i >= 4 ? 0xffffffffu : (1u << (8 * (old - i))) - 1u;
+            *p = (rescaled4(*p, had - b) & mask) | (*p & ~mask);
+          }
+      }
+      for (int slot = lo; slot < top; ++slot) {
+        const Source r = source(slot);
+        if (r.at < 0) continue;
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+          uint32_t x = codes[r.at + (int64_t)(lane + 64 * j) * page + r.off];
+          if (r.b != b) x = rescaled4(x, r.b - b);
+          dst[(lane + 64 * j) * page + (slot & (page - 1))] = (uint8_t)x;
+        }
+      }
+      if (lane == 0 && b != had) exps[th] = (uint8_t)b;
+    }
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_compact(const CompactArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const CacheLayer& layer = a.layer[blockIdx.y];
+  const int64_t items = (int64_t)a.kv.seqs * a.kv.kv_heads * 2;
+  for (int64_t i = (int64_t)blockIdx.x * 4 + wave; i < items; i += (int64_t)gridDim.x * 4) {
+    const int part = (int)(i % (2 * a.kv.kv_heads)), s = (int)(i / (2 * a.kv.kv_heads));
+    compact_item<D>(a, layer, s, part >> 1, part & 1, lane, part == 0 && blockIdx.y == 0 && a.len_out);
+  }
+}
+
+// ---------------------------------------------------------------------- fork
+constexpr int kForkThreads = 1024, kForkWaves = kForkThreads / 64;
+constexpr int kNew = -2;           // an entry that waits for its page
+
+// Every thread's v summed over those before it; `all` receives the whole.
+__device__ __forceinline__ int block_scan(int v, int* red, int* all) {
+  const int wave = threadIdx.x >> 6, incl = wave_incl_scan(v);
+  __syncthreads();                 // red is read
+  if ((threadIdx.x & 63) == 63) red[wave] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kForkWaves; ++w) {
+    before += w < wave ? red[w] : 0;
+    total += red[w];
+  }
+  *all = total;
+  return before + incl - v;
+}
+// What the workgroup's threads wrote, atomics included, is what they read behind this.
+__device__ __forceinline__ void meet_all() {
+  __threadfence();
+  __syncthreads();
+  __threadfence();
+}
+
+struct Row {
+  int parent, len, full, need;     // parent -1: an empty sequence
+};
+__device__ __forceinline__ Row row_of(const ForkArgs& a, int s) {
+  Row r{a.parent[s], 0, 0, 0};
+  if (r.parent < 0 || r.parent >= a.seqs) return Row{-1, 0, 0, 0};
+  const int64_t cap = (int64_t)a.max_pages * a.page;
+  const int len = a.kv_len[r.parent];
+  r.len = len < 0 ? 0 : (len < cap ? len : (int)cap);
+  r.full = r.len / a.page;
+  const int64_t need = (r.len + a.room + a.page - 1) / a.page;
+  r.need = need < a.max_pages ? (int)need : a.max_pages;
+  return r;
+}
+
+__global__ __launch_bounds__(kForkThreads) void k_kv_fork(const ForkArgs a) {
+  __shared__ int red[kForkWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i < a.num_pages; i += kForkThreads) a.refs_out[i] = a.refs[i];
+  for (int i = tid; i < a.seqs; i += kForkThreads) a.first[i] = a.outs;
+  meet_all();
+  for (int s = tid; s < a.outs; s += kForkThreads) {
+    const int p = a.parent[s];
+    if (p >= 0 && p < a.seqs) atomicMin(&a.first[p], s);
+  }
+  meet_all();
+  // pages let go, and those that rows hold without a new one
+  for (int64_t i = tid; i < (int64_t)a.seqs * a.max_pages; i += kForkThreads) {
+    const int e = a.table[i];
+    if (e >= 0 && e < a.num_pages) atomicAdd(&a.refs_out[e], -1);
+  }
+  for (int s = wave; s < a.outs; s += kForkWaves) {
+    const Row r = row_of(a, s);
+    const bool heir = r.parent >= 0 && a.first[r.parent] == s;
+    const int32_t* const from = a.table + (int64_t)(r.parent < 0 ? 0 : r.parent) * a.max_pages;
+    int fresh = 0;
+    for (int j0 = 0; j0 < a.max_pages; j0 += 64) {
+      const int j = j0 + lane;
+      int e = -1;
+      bool is_new = false;
+      if (j < r.need) {
+        e = from[j];
+        e = e >= 0 && e < a.num_pages ? e : -1;
+        if (j >= r.full && !(heir && e >= 0 && a.refs[e] == 1)) {
+          is_new = true;
+          if (j == r.full && r.len % a.page != 0 && e >= 0) atomicAdd(&a.refs_out[e], 1);     // held until it is copied
+        } else if (e >= 0) {
+          atomicAdd(&a.refs_out[e], 1);
+        }
+      }
+      if (j < a.max_pages) a.table_out[(int64_t)s * a.max_pages + j] = is_new ? kNew : e;
+      fresh += __builtin_popcountll(__ballot(is_new));
+    }
+    if (lane == 0) a.fresh[s] = fresh;
+  }
+  meet_all();
+  // new pages are numbered by row and entry
+  int all = 0;
+  for (int base = 0; base < a.outs; base += kForkThreads) {
+    const int s = base + tid, n = s < a.outs ? a.fresh[s] : 0;
+    int sum;
+    const int before = block_scan(n, red, &sum);
+    if (s < a.outs) a.fresh[s] = all + before;
+    all += sum;
+  }
+  // and taken from the lowest free ones
+  int found = 0;
+  for (int64_t base = 0; base < a.num_pages && found < all; base += kForkThreads) {
+    const int64_t p = base + tid;
+    const bool free = p < a.num_pages && a.refs_out[p] == 0;
+    int sum;
+    const int at = found + block_scan(free ? 1 : 0, red, &sum);
+    if (free && at < all) {
+      a.taken[at] = (int)p;
+      a.refs_out[p] = 1;
+    }
+    found += sum;
+  }
+  meet_all();
+  for (int s = wave; s < a.outs; s += kForkWaves) {
+    const Row r = row_of(a, s);
+    int at = a.fresh[s], src = -1, dst = -1, len = r.len;
+    for (int j0 = 0; j0 < r.need; j0 += 64) {
+      const int j = j0 + lane;
+      int32_t* const entry = a.table_out + (int64_t)s * a.max_pages + j;
+      const bool is_new = j < r.need && *entry == kNew;
+      const uint64_t news = __ballot(is_new);
+      if (is_new) {
+        const int rank = at + __builtin_popcountll(news & (((uint64_t)1 << lane) - 1));
+        const int page = rank < found && rank < all ? a.taken[rank] : -1;
+        *entry = page;
+        if (j == r.full && r.len % a.page != 0) {
+          const int e = a.table[(int64_t)r.parent * a.max_pages + j];
+          if (page < 0) len = r.full * a.page;
+          if (e >= 0 && e < a.num_pages) {
+            atomicAdd(&a.refs_out[e], -1);
+            if (page >= 0) {
+              src = e;
+              dst = page;
+            }
+          }
+        }
+      }
+      at += __builtin_popcountll(news);
+    }
+    // the lane of the open page has the word
+    const uint64_t copies = __ballot(src >= 0), cut = __ballot(len != r.len);
+    const int who = copies ? __builtin_ctzll(copies) : 0;
+    src = __builtin_amdgcn_readlane(src, who);
+    dst = __builtin_amdgcn_readlane(dst, who);
+    if (lane == 0) {
+      a.len_out[s] = cut ? r.full * a.page : r.len;
+      a.copies[2 * s] = copies ? src : -1;
+      a.copies[2 * s + 1] = copies ? dst : -1;
+    }
+  }
+  if (tid == 0) *a.missing = all > found ? all - found : 0;
+}
+
+// Slices of 16 KB of a page's keys and values in every layer
+constexpr int kSlice = 16384;
+__global__ __launch_bounds__(256) void k_copy_pages(const ForkArgs a, int layers, int slices) {
+  const int tid = threadIdx.x;
+  const int64_t bytes = a.page_bytes, items = (int64_t)a.outs * layers * slices;
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int slice = (int)(i % slices), l = (int)(i / slices % layers), s = (int)(i / slices / layers);
+    const int src = a.copies[2 * s], dst = a.copies[2 * s + 1];
+    if (src < 0) continue;
+    const CacheLayer& c = a.layer[l];
+    if (slice == 0)
+      for (int h = tid; h < 2 * a.kv_heads; h += 256) {
+        uint8_t* const e = h < a.kv_heads ? c.ke : c.ve;
+        const int hh = h < a.kv_heads ? h : h - a.kv_heads;
+        e[(int64_t)dst * a.kv_heads + hh] = e[(int64_t)src * a.kv_heads + hh];
+      }
+    const int64_t lo = (int64_t)slice * kSlice, hi = lo + kSlice < 2 * bytes ? lo + kSlice : 2 * bytes;
+#pragma unroll 4
+    for (int64_t o = lo + 16 * tid; o < hi; o += 16 * 256) {
+      uint8_t* const base = o < bytes ? c.k : c.v;
+      const int64_t off = o < bytes ? o : o - bytes;
+      *(v4i*)(base + (int64_t)dst * bytes + off) = *(const v4i*)(base + (int64_t)src * bytes + off);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_compact(const CompactArgs& a, int dim, int layers, hipStream_t st) {
+  const int64_t items = (int64_t)a.kv.seqs * a.kv.kv_heads * 2, blocks = (items + 3) / 4;
+  const dim3 grid((unsigned)(blocks < (1 << 22) ? blocks : 1 << 22), (unsigned)layers);
+  switch (dim) {
+    case 64: k_kv_compact<64><<<grid, 256, 0, st>>>(a); break;
+    case 128: k_kv_compact<128><<<grid, 256, 0, st>>>(a); break;
+    default: k_kv_compact<256><<<grid, 256, 0, st>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t st) {
+  k_kv_fork<<<1, kForkThreads, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_copy_pages(const ForkArgs& a, int layers, hipStream_t st) {
+  const int slices = (int)((2 * a.page_bytes + kSlice - 1) / kSlice);
+  const int64_t items = (int64_t)a.outs * layers * slices;
+  k_copy_pages<<<(unsigned)(items < 16384 ? items : 16384), 256, 0, st>>>(a, layers, slices);
+  return hipGetLastError();
+}
+
+}  // namespace q8

@@ -568,6 +568,69 @@ def q8_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatc
     return out
 
 
+def q8_kv_append_norm(k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatch,
+                      q: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                      k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, cos: Optional[torch.Tensor] = None,
+                      sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                      positions: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """q8_kv_append with each head of k and q divided by the root of its mean square (plus eps)
+    and multiplied by k_weight, q_weight [dim] (float32, float16 or bfloat16, of one dtype; None:
+    that side is left as it is) before the rotation, which goes by positions (int32 [T]) where
+    they are given, as for drafted tokens, and else by the tokens' slots."""
+    r = _fast().kv_append_norm(k, v, cache, batch, q, q_weight, k_weight, eps, cos, sin, interleaved, positions, out)
+    if r is not NotImplemented:
+        return _result("q8_kv_append_norm", r)
+    index, dev = _cuda_index(k, "k"), k.device
+    P, Hkv, page, D, S, max_pages = _check_kv(cache, batch, dev, index)
+    dt = k.dtype
+    k_step = _rows(k, "k", dt, (Hkv, D), index)
+    v_step = _rows(v, "v", dt, (Hkv, D), index)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"v must have {T} tokens, got {v.shape[0]}")
+    Hq = q_step = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        q_step = _rows(q, "q", dt, (Hq, D), index)
+        if q.shape[0] != T:
+            raise ValueError(f"q must have {T} tokens, got {q.shape[0]}")
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        else:
+            _need(out, "out", dt, (T, Hq, D), dev)
+    elif out is not None:
+        raise ValueError("out is given without q")
+    elif q_weight is not None:
+        raise ValueError("q_weight is given without q")
+    wd = torch.float32
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            wd = w.dtype if name == "q_weight" or q_weight is None else wd
+            _need(w, name, wd, (D,), dev)
+    if positions is not None:
+        _need(positions, "positions", _I32, (T,), dev)
+    angles = rot = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos must be 2-D [positions, rot_dim / 2]")
+        angles, half = shape = cos.shape
+        rot = 2 * half
+        _need(cos, "cos", torch.float32, None, dev)
+        _need(sin, "sin", torch.float32, shape, dev)
+    with torch.cuda.device(index):
+        st = _lib.lib().q8_kv_append_norm(
+            _ptr(q), q_step, k.data_ptr(), k_step, v.data_ptr(), v_step, _DT[dt], T, Hq, Hkv, D, _ptr(q_weight),
+            _ptr(k_weight), _DT[wd], eps, _ptr(cos), _ptr(sin), angles, rot, interleaved, _ptr(positions),
+            batch.q_start.data_ptr(), batch.kv_len.data_ptr(), batch.block_table.data_ptr(), S, max_pages, batch.max_q,
+            cache.k.data_ptr(), cache.k_exp.data_ptr(), cache.v.data_ptr(), cache.v_exp.data_ptr(), P, page, _ptr(out),
+            _raw_stream(index))
+    _lib.check("q8_kv_append_norm", st)
+    return out
+
+
 def q8_attention_workspace_bytes(T: int, heads: int, kv_heads: int, dim: int, seqs: int, max_q: int, max_kv: int,
                                  window: int = 0) -> int:
     return int(_lib.lib().q8_attention_workspace_bytes(T, heads, kv_heads, dim, seqs, max_q, max_kv, window))
@@ -615,6 +678,152 @@ def q8_attention_kv8(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Opt
     if st:
         _lib.check("q8_attention_kv8", st)
     return (y, le) if lse else y
+
+
+def q8_attention_kv8_tree(q: torch.Tensor, cache: KvCache, batch: KvBatch, mask: torch.Tensor,
+                          positions: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
+                          lse: bool = False, out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None):
+    """q8_attention_kv8 of drafted tokens: a new token sees the cached keys (with a window: those
+    that its position, an int32 of positions [T], reaches back to) and the new tokens of its
+    sequence whose bit is set in its row of mask (int64 or uint64 [T, words], bit j % 64 of word
+    j / 64 for new token j).  Returns out [T, heads, dim] (and the log-sum-exp if lse)."""
+    if not lse and workspace is None:
+        r = _fast().attention_kv8_tree(q, cache, batch, mask, positions, scale, window, out)
+        if r is not NotImplemented:
+            return _result("q8_attention_kv8_tree", r)
+    index, dev = _cuda_index(q, "q"), q.device
+    P, Hkv, page, D, S, max_pages = _check_kv(cache, batch, dev, index)
+    dt = q.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise TypeError("q8_attention_kv8_tree: q must be bfloat16 or float16")
+    T, Hq = q.shape[:2] if q.dim() == 3 else (0, 0)
+    q_step = _rows(q, "q", dt, (Hq, D), index)
+    if mask.dim() != 2 or mask.dtype not in (torch.int64, torch.uint64):
+        raise TypeError("mask must be 2-D int64 or uint64 [tokens, words]")
+    words = mask.shape[1]
+    _need(mask, "mask", mask.dtype, (T, words), dev)
+    if positions is not None:
+        _need(positions, "positions", _I32, (T,), dev)
+    y = torch.empty((T, Hq, D), dtype=dt, device=dev) if out is None else out
+    _need(y, "out", dt, (T, Hq, D), dev)
+    le = torch.empty(T, Hq, dtype=torch.float32, device=dev) if lse else None
+    L = _lib.lib()
+    ws, wsn = workspace, 0
+    if ws is None:
+        wsn = L.q8_attention_workspace_bytes(T, Hq, Hkv, D, S, batch.max_q, batch.max_kv, window)
+        if wsn:
+            ws = torch.empty(wsn, dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, "workspace", None, None, dev)
+        wsn = ws.nbytes
+    with torch.cuda.device(index):
+        st = L.q8_attention_kv8_tree(
+            q.data_ptr(), q_step, _DT[dt], T, Hq, Hkv, D, batch.q_start.data_ptr(), batch.kv_len.data_ptr(),
+            batch.block_table.data_ptr(), S, max_pages, batch.max_q, batch.max_kv, cache.k.data_ptr(),
+            cache.k_exp.data_ptr(), cache.v.data_ptr(), cache.v_exp.data_ptr(), P, page, mask.data_ptr(), words,
+            _ptr(positions), 1.0 / math.sqrt(D) if scale is None else scale, window, y.data_ptr(), _ptr(le), _ptr(ws),
+            wsn, _raw_stream(index))
+    _lib.check("q8_attention_kv8_tree", st)
+    return (y, le) if lse else y
+
+
+def _layers(caches, dev=None):
+    """The caches of all layers, a KvCache or a sequence of them (4-tuples in its order), checked to be
+    alike, as ctypes arrays of their pointers; and (pages, kv_heads, page, dim, device)."""
+    if isinstance(caches, tuple) and len(caches) == 4 and isinstance(caches[0], torch.Tensor):
+        caches = (caches,)
+    caches = [KvCache(*c) for c in caches]
+    if not caches:
+        raise ValueError("caches must hold the cache of one layer at least")
+    k = caches[0].k
+    dev = k.device if dev is None else dev
+    if k.dim() != 4 or k.dtype not in _CODES:
+        raise ValueError("caches[0].k must be 4-D uint8 or float8_e4m3fn")
+    P, Hkv, page, D = k.shape
+    shapes = ((P, Hkv, page, D), (P, Hkv), (P, Hkv, D, page), (P, Hkv))
+    for i, c in enumerate(caches):
+        for t, name, shape, kinds in zip(c, KvCache._fields, shapes, (_CODES, _EXPS, _CODES, _EXPS)):
+            _need(t, f"caches[{i}].{name}", None, shape, dev)
+            if t.dtype not in kinds:
+                raise TypeError(f"caches[{i}].{name} must be {kinds[0]} or {kinds[1]}, got {t.dtype}")
+    arrays = [(ctypes.c_void_p * len(caches))(*(c[i].data_ptr() for c in caches)) for i in range(4)]
+    return arrays, len(caches), P, Hkv, page, D, dev
+
+
+def q8_kv_compact(caches, batch: KvBatch, keep: torch.Tensor, n_keep: torch.Tensor,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The drafts that are kept go to the front of their slots, in the caches of all layers (a
+    KvCache or a sequence of them that share batch.block_table): new token keep[s, i] of sequence s
+    becomes its new token i, for i < n_keep[s] (int32 [S, max_keep], growing, and [S]).  Returns the
+    lengths with the kept tokens, int32 [S]."""
+    r = _fast().kv_compact(caches, batch, keep, n_keep, out)
+    if r is not NotImplemented:
+        return _result("q8_kv_compact", r)
+    arrays, layers, P, Hkv, page, D, dev = _layers(caches)
+    start, lens, table = batch[:3]
+    if table.dim() != 2 or keep.dim() != 2:
+        raise ValueError("batch.block_table and keep must be 2-D")
+    S, max_pages = table.shape
+    _need(table, "batch.block_table", _I32, None, dev)
+    _need(start, "batch.q_start", _I32, (S + 1,), dev)
+    _need(lens, "batch.kv_len", _I32, (S,), dev)
+    _need(keep, "keep", _I32, (S, keep.shape[1]), dev)
+    _need(n_keep, "n_keep", _I32, (S,), dev)
+    y = torch.empty_like(lens) if out is None else out
+    _need(y, "out", _I32, (S,), dev)
+    with torch.cuda.device(dev):
+        st = _lib.lib().q8_kv_compact(*arrays, layers, Hkv, D, _ptr(start), _ptr(lens), _ptr(table), S, max_pages, P, page,
+                                      _ptr(keep), keep.shape[1], _ptr(n_keep), _ptr(y), _raw_stream(dev.index))
+    _lib.check("q8_kv_compact", st)
+    return y
+
+
+class KvFork(NamedTuple):
+    """What q8_kv_fork returns: the new batch's block table [S_out, max_pages] and lengths [S_out], the
+    pages' counts [pages], and how many pages were missing [1] (int32)."""
+    block_table: torch.Tensor
+    kv_len: torch.Tensor
+    refs: torch.Tensor
+    missing: torch.Tensor
+
+
+def q8_kv_fork_workspace_bytes(seqs: int, outs: int, pages: int) -> int:
+    return int(_lib.lib().q8_kv_fork_workspace_bytes(seqs, outs, pages))
+
+
+def q8_kv_fork(caches, block_table: torch.Tensor, kv_len: torch.Tensor, refs: torch.Tensor, parent: torch.Tensor,
+               room: int = 0, out: Optional[KvFork] = None, workspace: Optional[torch.Tensor] = None) -> KvFork:
+    """A batch whose sequence s continues parent[s] (int32 [S_out]; outside the old batch: empty) of the
+    batch block_table [S, max_pages], kv_len [S], with pages for `room` more tokens: full pages are
+    shared, open ones copied in the caches of all layers for all but the first that continues a sequence,
+    new pages taken from the lowest free ones; refs [pages] counts the entries that hold a page (0: free).
+    The old table's entries are let go.  Returns a KvFork (`out`: given tensors for it)."""
+    r = _fast().kv_fork(caches, block_table, kv_len, refs, parent, room, out, workspace)
+    if r is not NotImplemented:
+        return KvFork(*r) if type(r) is tuple else _result("q8_kv_fork", r)
+    arrays, layers, P, Hkv, page, D, dev = _layers(caches)
+    if block_table.dim() != 2 or parent.dim() != 1:
+        raise ValueError("block_table must be 2-D and parent 1-D")
+    (S, max_pages), outs = block_table.shape, parent.shape[0]
+    _need(block_table, "block_table", _I32, None, dev)
+    _need(kv_len, "kv_len", _I32, (S,), dev)
+    _need(refs, "refs", _I32, (P,), dev)
+    _need(parent, "parent", _I32, None, dev)
+    shapes = ((outs, max_pages), (outs,), (P,), (1,))
+    y = KvFork(*(torch.empty(n, dtype=_I32, device=dev) for n in shapes)) if out is None else KvFork(*out)
+    for t, name, shape in zip(y, KvFork._fields, shapes):
+        _need(t, f"out.{name}", _I32, shape, dev)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(max(1, q8_kv_fork_workspace_bytes(S, outs, P)), dtype=torch.uint8, device=dev)
+    _need(ws, "workspace", None, None, dev)
+    with torch.cuda.device(dev):
+        st = _lib.lib().q8_kv_fork(*arrays, layers, Hkv, D, P, page, _ptr(block_table), _ptr(kv_len), _ptr(refs), S,
+                                   max_pages, _ptr(parent), outs, room, *(_ptr(t) for t in y), _ptr(ws), ws.nbytes,
+                                   _raw_stream(dev.index))
+    _lib.check("q8_kv_fork", st)
+    return y
 
 
 def _need_codes(t: torch.Tensor, name: str, shape=None, dev=None) -> None:
