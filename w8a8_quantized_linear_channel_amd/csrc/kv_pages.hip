@@ -74,6 +74,23 @@ __device__ __forceinline__ int path_of(const int32_t* keep, int most, int n, int
   return total;
 }
 
+// Byte e of a word as a value
+template <int E>
+__device__ __forceinline__ float value_of(uint32_t w) { return __builtin_amdgcn_cvt_f32_fp8((int)w, E); }
+
+// Four codes, each times a power of two of its own, NaN codes as they are
+__device__ __forceinline__ uint32_t rescaled4(uint32_t w, const int* shift) {
+  const uint32_t t = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u, nan = (t << 1) - (t >> 7);
+  return (pack4_e4m3(__builtin_ldexpf(value_of<0>(w), shift[0]), __builtin_ldexpf(value_of<1>(w), shift[1]),
+                     __builtin_ldexpf(value_of<2>(w), shift[2]), __builtin_ldexpf(value_of<3>(w), shift[3])) & ~nan) | (w & nan);
+}
+
+// Where a page's tokens come from, token i at lane i % 64 of one of two sets (a page has 128 tokens at
+// most): page x head, -1 without one; place in that page, and its exponent byte << 8.
+struct Sources {
+  int ph[2], at[2];
+};
+
 template <int D>
 __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int s, int head, bool is_v, int lane, bool says) {
   const KvView& kv = a.kv;
@@ -98,112 +115,167 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
   auto page_at = [&](int slot) {
     if (slot < 0 || slot >= cap) return -1;
     const int p = table[slot >> page_log2];
-    return p < kv.num_pages ? p : -1;
+    return p >= 0 && p < kv.num_pages ? p : -1;
   };
   for (; lo < hi; lo = (lo & ~(page - 1)) + page) {
-    const int stop = (lo & ~(page - 1)) + page, top = hi < stop ? hi : stop;
+    const int stop = (lo & ~(page - 1)) + page, top = hi < stop ? hi : stop, count = top - lo;
+    // the sources of all tokens in one go, a token a lane
+    Sources from{{-1, -1}, {0, 0}};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 64 * h + lane;
+      if (i >= count) continue;
+      const int slot = past + keep[lo + i - past], p = page_at(slot);
+      if (p < 0) continue;
+      from.ph[h] = p * kv.kv_heads + head;
+      from.at[h] = (slot & (page - 1)) | (int)exps[from.ph[h]] << 8;
+    }
     const int to = page_at(lo);
     if (to < 0) continue;
     const int64_t th = (int64_t)to * kv.kv_heads + head;
     uint8_t* const dst = codes + th * page * D;
-    const int had = exps[th];
-    const bool fresh = (lo & (page - 1)) == 0;
-    // a token's source: offset of its head's codes, place in the page and exponent byte; -1 without one
-    struct Source {
-      int64_t at;
-      int off, b;
-    };
-    auto source = [&](int slot) {
-      Source r{-1, 0, 0};
-      const int from = past + keep[slot - past], p = page_at(from);
-      if (p < 0) return r;
-      const int64_t ph = (int64_t)p * kv.kv_heads + head;
-      r.at = ph * page * D;
-      r.off = from & (page - 1);
-      r.b = exps[ph];
-      return r;
-    };
+    const int had = exps[th], old = lo & (page - 1);
+    const bool fresh = old == 0;
     int want = -1;
-    auto settle = [&]() {            // the page's new byte, -1 where nothing comes
+    auto settle = [&] {              // the page's new byte, -1 where nothing comes
       want = wave_max_i(want);
       return want < 0 ? -1 : (fresh || want > had ? want : had);
     };
     if (!is_v) {
-      constexpr int C = D / 16, G = 64 / C;         // chunks of a token, tokens at once
+      // 16 features a lane, G tokens at once; U of those in registers
+      constexpr int C = D / 16, G = 64 / C, U = 4;
       const int c = lane % C;
-      auto load = [&](int slot, Source& r, v4i& x) {
-        r = source(slot);
-        x = r.at >= 0 ? *(const v4i*)(codes + r.at + r.off * D + 16 * c) : v4i{0, 0, 0, 0};
+      v4i x[U];
+      int at[U];                     // -1: nothing
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * G + lane / C;
+          int ph = __shfl(from.ph[0], i & 63);
+          at[u] = __shfl(from.at[0], i & 63);
+          if (page > 64) {
+            const int p1 = __shfl(from.ph[1], i & 63), a1 = __shfl(from.at[1], i & 63);
+            ph = i < 64 ? ph : p1;
+            at[u] = i < 64 ? at[u] : a1;
+          }
+          at[u] = i < count && ph >= 0 ? at[u] : -1;
+          x[u] = v4i{0, 0, 0, 0};
+          if (at[u] >= 0) x[u] = *(const v4i*)(codes + ((int64_t)ph * page + (at[u] & 255)) * D + 16 * c);
+        }
       };
-      Source r0{-1, 0, 0};
-      v4i x0 = {0, 0, 0, 0};
-      for (int slot = lo + lane / C; slot < top; slot += G) {
-        Source r;
-        v4i x;
-        load(slot, r, x);
-        if (r.at < 0) continue;
-        int big = 0;
+      for (int i0 = 0; i0 < count; i0 += U * G) {
+        load(i0);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) big = largest4((uint32_t)x[w], big);
-        const int w = wanted(big, r.b);
-        want = w > want ? w : want;
-        if (slot < lo + G) {
-          r0 = r;
-          x0 = x;
-        }
-      }
-      const int b = settle();
-      if (b < 0) continue;
-      if (!fresh && b != had)
-        for (int i = lane / C; i < (lo & (page - 1)); i += G) {
-          v4i* const p = (v4i*)(dst + i * D + 16 * c);
-          v4i x = *p;
+        for (int u = 0; u < U; ++u) {
+          if (at[u] < 0) continue;
+          int big = 0;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) x[w] = (int)rescaled4((uint32_t)x[w], had - b);
-          *p = x;
-        }
-      for (int slot = lo + lane / C; slot < top; slot += G) {
-        Source r = r0;
-        v4i x = x0;
-        if (slot >= lo + G) load(slot, r, x);
-        if (r.at < 0) continue;
-        if (r.b != b)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) x[w] = (int)rescaled4((uint32_t)x[w], r.b - b);
-        *(v4i*)(dst + (slot & (page - 1)) * D + 16 * c) = x;
-      }
-      if (lane == 0 && b != had) exps[th] = (uint8_t)b;
-    } else {
-      constexpr int F = D / 64;                     // features of a lane
-      for (int slot = lo; slot < top; ++slot) {
-        const Source r = source(slot);
-        if (r.at < 0) continue;
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
-          const int w = wanted(codes[r.at + (int64_t)(lane + 64 * j) * page + r.off], r.b);
+          for (int w = 0; w < 4; ++w) big = largest4((uint32_t)x[u][w], big);
+          const int w = wanted(big, at[u] >> 8);
           want = w > want ? w : want;
         }
       }
       const int b = settle();
       if (b < 0) continue;
-      if (!fresh && b != had) {
-        const int old = lo & (page - 1);
+      if (!fresh && b != had)
+        for (int i = lane / C; i < old; i += G) {
+          v4i* const p = (v4i*)(dst + i * D + 16 * c);
+          v4i y = *p;
 #pragma unroll
-        for (int j = 0; j < F; ++j)
-          for (int i = 0; i < old; i += 4) {
-            uint32_t* const p = (uint32_t*)(dst + (lane + 64 * j) * page + i);
-            const uint32_t mask = old - i >= 4 ? 0xffffffffu : (1u << (8 * (old - i))) - 1u;
-            *p = (rescaled4(*p, had - b) & mask) | (*p & ~mask);
+          for (int w = 0; w < 4; ++w) y[w] = (int)rescaled4((uint32_t)y[w], had - b);
+          *p = y;
+        }
+      for (int i0 = 0; i0 < count; i0 += U * G) {
+        if (count > U * G) load(i0);               // (else they are there)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (at[u] < 0) continue;
+          const int shift = (at[u] >> 8) - b;
+          if (shift != 0)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x[u][w] = (int)rescaled4((uint32_t)x[u][w], shift);
+          *(v4i*)(dst + (old + i0 + u * G + lane / C) * D + 16 * c) = x[u];
+        }
+      }
+      if (lane == 0 && b != had) exps[th] = (uint8_t)b;
+    } else {
+      // D / 64 features a lane, U words of four tokens in registers
+      constexpr int F = D / 64, U = 2;
+      const int w0 = old & ~3, words = (old + count - w0 + 3) / 4;
+      uint32_t x[U][F], was[U][F];
+      int shift[U][4];               // byte of the token's page; -1: not a new token
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int j = 0; j < F; ++j) {
+            x[u][j] = 0;
+            was[u][j] = i0 + u < words ? *(const uint32_t*)(dst + (lane + 64 * j) * page + w0 + 4 * (i0 + u)) : 0;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = w0 + 4 * (i0 + u) + e - old;       // uniform
+            shift[u][e] = -1;
+            if (i < 0 || i >= count) continue;
+            const int ph = __builtin_amdgcn_readlane(i < 64 ? from.ph[0] : from.ph[1], i & 63);
+            const int at = __builtin_amdgcn_readlane(i < 64 ? from.at[0] : from.at[1], i & 63);
+            if (ph < 0) continue;
+            shift[u][e] = at >> 8;
+            const uint8_t* const p = codes + (int64_t)ph * page * D + (at & 255);
+#pragma unroll
+            for (int j = 0; j < F; ++j) x[u][j] |= (uint32_t)p[(lane + 64 * j) * page] << (8 * e);
+          }
+        }
+      };
+      for (int i0 = 0; i0 < words; i0 += U) {
+        load(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (shift[u][e] < 0) continue;
+#pragma unroll
+            for (int j = 0; j < F; ++j) {
+              const int w = wanted((int)(x[u][j] >> (8 * e)), shift[u][e]);
+              want = w > want ? w : want;
+            }
           }
       }
-      for (int slot = lo; slot < top; ++slot) {
-        const Source r = source(slot);
-        if (r.at < 0) continue;
+      const int b = settle();
+      if (b < 0) continue;
+      if (!fresh && b != had)
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-          uint32_t x = codes[r.at + (int64_t)(lane + 64 * j) * page + r.off];
-          if (r.b != b) x = rescaled4(x, r.b - b);
-          dst[(lane + 64 * j) * page + (slot & (page - 1))] = (uint8_t)x;
+        for (int j = 0; j < F; ++j)
+          for (int i = 0; i < w0; i += 4) {
+            uint32_t* const p = (uint32_t*)(dst + (lane + 64 * j) * page + i);
+            *p = rescaled4(*p, had - b);
+          }
+      for (int i0 = 0; i0 < words; i0 += U) {
+        if (words > U) load(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u >= words) continue;
+          // bytes of new tokens, those before them at the new scale, and what lies between and behind
+          uint32_t put = 0;
+          int by[4];
+          bool move = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool is_new = shift[u][e] >= 0, is_old = w0 + 4 * (i0 + u) + e < old;
+            put |= is_new || is_old ? 0xffu << (8 * e) : 0u;
+            by[e] = is_new ? shift[u][e] - b : (is_old ? had - b : 0);
+            move |= by[e] != 0;
+          }
+#pragma unroll
+          for (int j = 0; j < F; ++j) {
+            uint32_t y = x[u][j];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (shift[u][e] < 0) y |= was[u][j] & (0xffu << (8 * e));
+            if (move) y = rescaled4(y, by);
+            y = (y & put) | (was[u][j] & ~put);
+            *(uint32_t*)(dst + (lane + 64 * j) * page + w0 + 4 * (i0 + u)) = y;
+          }
         }
       }
       if (lane == 0 && b != had) exps[th] = (uint8_t)b;
@@ -241,11 +313,8 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* all) {
   *all = total;
   return before + incl - v;
 }
-// What the workgroup's threads wrote, atomics included, is what they read behind this.
-__device__ __forceinline__ void meet_all() {
-  __threadfence();
-  __syncthreads();
-  __threadfence();
+__device__ __forceinline__ void add_one(int* p, int v) {
+  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
 struct Row {
@@ -263,29 +332,41 @@ __device__ __forceinline__ Row row_of(const ForkArgs& a, int s) {
   return r;
 }
 
-__global__ __launch_bounds__(kForkThreads) void k_kv_fork(const ForkArgs a) {
+// LOCAL: counts and the rows' numbers in LDS (up to kForkPages pages and kForkRows rows of either batch),
+// else in the caller's arrays.  A row takes as many lanes as its entries need, up to 64.
+constexpr int kForkPages = 16384, kForkRows = 1024;
+template <bool LOCAL>
+__global__ __launch_bounds__(kForkThreads) void k_kv_fork(const ForkArgs a, int lanes) {
   __shared__ int red[kForkWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int i = tid; i < a.num_pages; i += kForkThreads) a.refs_out[i] = a.refs[i];
-  for (int i = tid; i < a.seqs; i += kForkThreads) a.first[i] = a.outs;
-  meet_all();
+  __shared__ int s_count[LOCAL ? kForkPages : 1], s_first[LOCAL ? kForkRows : 1], s_fresh[LOCAL ? kForkRows : 1];
+  int* const count = LOCAL ? s_count : a.refs_out;
+  int* const first = LOCAL ? s_first : a.first;
+  int* const fresh = LOCAL ? s_fresh : a.fresh;
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int i = tid; i < a.num_pages; i += kForkThreads) count[i] = a.refs[i];
+  for (int i = tid; i < a.seqs; i += kForkThreads) first[i] = a.outs;
+  __syncthreads();
   for (int s = tid; s < a.outs; s += kForkThreads) {
     const int p = a.parent[s];
-    if (p >= 0 && p < a.seqs) atomicMin(&a.first[p], s);
+    if (p >= 0 && p < a.seqs) __hip_atomic_fetch_min(&first[p], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
   }
-  meet_all();
-  // pages let go, and those that rows hold without a new one
+  // pages let go
   for (int64_t i = tid; i < (int64_t)a.seqs * a.max_pages; i += kForkThreads) {
     const int e = a.table[i];
-    if (e >= 0 && e < a.num_pages) atomicAdd(&a.refs_out[e], -1);
+    if (e >= 0 && e < a.num_pages) add_one(&count[e], -1);
   }
-  for (int s = wave; s < a.outs; s += kForkWaves) {
+  __syncthreads();
+  // those that rows hold without a new one; a row's lanes start at bit `base` of the wave's
+  const int mine = tid / lanes, rows = kForkThreads / lanes, col = tid % lanes, base = lane & ~(lanes - 1);
+  const uint64_t whole = lanes == 64 ? ~(uint64_t)0 : (((uint64_t)1 << lanes) - 1) << base;
+  const uint64_t below = whole & (((uint64_t)1 << lane) - 1);
+  for (int s = mine; s < a.outs; s += rows) {
     const Row r = row_of(a, s);
-    const bool heir = r.parent >= 0 && a.first[r.parent] == s;
+    const bool heir = r.parent >= 0 && first[r.parent] == s;
     const int32_t* const from = a.table + (int64_t)(r.parent < 0 ? 0 : r.parent) * a.max_pages;
-    int fresh = 0;
-    for (int j0 = 0; j0 < a.max_pages; j0 += 64) {
-      const int j = j0 + lane;
+    int news = 0;
+    for (int j0 = 0; j0 < a.max_pages; j0 += lanes) {
+      const int j = j0 + col;
       int e = -1;
       bool is_new = false;
       if (j < r.need) {
@@ -293,78 +374,78 @@ __global__ __launch_bounds__(kForkThreads) void k_kv_fork(const ForkArgs a) {
         e = e >= 0 && e < a.num_pages ? e : -1;
         if (j >= r.full && !(heir && e >= 0 && a.refs[e] == 1)) {
           is_new = true;
-          if (j == r.full && r.len % a.page != 0 && e >= 0) atomicAdd(&a.refs_out[e], 1);     // held until it is copied
+          if (j == r.full && r.len % a.page != 0 && e >= 0) add_one(&count[e], 1);     // held until it is copied
         } else if (e >= 0) {
-          atomicAdd(&a.refs_out[e], 1);
+          add_one(&count[e], 1);
         }
       }
       if (j < a.max_pages) a.table_out[(int64_t)s * a.max_pages + j] = is_new ? kNew : e;
-      fresh += __builtin_popcountll(__ballot(is_new));
+      news += __builtin_popcountll(__ballot(is_new) & whole);
     }
-    if (lane == 0) a.fresh[s] = fresh;
+    if (col == 0) fresh[s] = news;
   }
-  meet_all();
+  __syncthreads();
   // new pages are numbered by row and entry
   int all = 0;
-  for (int base = 0; base < a.outs; base += kForkThreads) {
-    const int s = base + tid, n = s < a.outs ? a.fresh[s] : 0;
+  for (int at = 0; at < a.outs; at += kForkThreads) {
+    const int s = at + tid, n = s < a.outs ? fresh[s] : 0;
     int sum;
     const int before = block_scan(n, red, &sum);
-    if (s < a.outs) a.fresh[s] = all + before;
+    if (s < a.outs) fresh[s] = all + before;
     all += sum;
   }
   // and taken from the lowest free ones
   int found = 0;
-  for (int64_t base = 0; base < a.num_pages && found < all; base += kForkThreads) {
-    const int64_t p = base + tid;
-    const bool free = p < a.num_pages && a.refs_out[p] == 0;
+  for (int64_t at = 0; at < a.num_pages && found < all; at += kForkThreads) {
+    const int64_t p = at + tid;
+    const bool free = p < a.num_pages && count[p] == 0;
     int sum;
-    const int at = found + block_scan(free ? 1 : 0, red, &sum);
-    if (free && at < all) {
-      a.taken[at] = (int)p;
-      a.refs_out[p] = 1;
+    const int rank = found + block_scan(free ? 1 : 0, red, &sum);
+    if (free && rank < all) {
+      a.taken[rank] = (int)p;
+      count[p] = 1;
     }
     found += sum;
   }
-  meet_all();
-  for (int s = wave; s < a.outs; s += kForkWaves) {
+  __syncthreads();
+  for (int s = mine; s < a.outs; s += rows) {
     const Row r = row_of(a, s);
-    int at = a.fresh[s], src = -1, dst = -1, len = r.len;
-    for (int j0 = 0; j0 < r.need; j0 += 64) {
-      const int j = j0 + lane;
+    int at = fresh[s], src = -1, dst = -1;
+    bool cut = false;
+    for (int j0 = 0; j0 < r.need; j0 += lanes) {
+      const int j = j0 + col;
       int32_t* const entry = a.table_out + (int64_t)s * a.max_pages + j;
       const bool is_new = j < r.need && *entry == kNew;
       const uint64_t news = __ballot(is_new);
       if (is_new) {
-        const int rank = at + __builtin_popcountll(news & (((uint64_t)1 << lane) - 1));
+        const int rank = at + __builtin_popcountll(news & below);
         const int page = rank < found && rank < all ? a.taken[rank] : -1;
         *entry = page;
         if (j == r.full && r.len % a.page != 0) {
           const int e = a.table[(int64_t)r.parent * a.max_pages + j];
-          if (page < 0) len = r.full * a.page;
+          cut = page < 0;
           if (e >= 0 && e < a.num_pages) {
-            atomicAdd(&a.refs_out[e], -1);
-            if (page >= 0) {
-              src = e;
-              dst = page;
-            }
+            add_one(&count[e], -1);
+            src = page >= 0 ? e : -1;
+            dst = page;
           }
         }
       }
-      at += __builtin_popcountll(news);
+      at += __builtin_popcountll(news & whole);
     }
-    // the lane of the open page has the word
-    const uint64_t copies = __ballot(src >= 0), cut = __ballot(len != r.len);
-    const int who = copies ? __builtin_ctzll(copies) : 0;
-    src = __builtin_amdgcn_readlane(src, who);
-    dst = __builtin_amdgcn_readlane(dst, who);
-    if (lane == 0) {
-      a.len_out[s] = cut ? r.full * a.page : r.len;
-      a.copies[2 * s] = copies ? src : -1;
-      a.copies[2 * s + 1] = copies ? dst : -1;
+    // the lane of the open page has the word, the row's first lane where it has none
+    const uint64_t copies = __ballot(src >= 0) & whole, cuts = __ballot(cut) & whole;
+    if (copies ? src >= 0 : col == 0) {
+      a.len_out[s] = cuts ? r.full * a.page : r.len;
+      a.copies[2 * s] = src;
+      a.copies[2 * s + 1] = dst;
     }
   }
   if (tid == 0) *a.missing = all > found ? all - found : 0;
+  if constexpr (LOCAL) {
+    __syncthreads();
+    for (int i = tid; i < a.num_pages; i += kForkThreads) a.refs_out[i] = count[i];
+  }
 }
 
 // Slices of 16 KB of a page's keys and values in every layer
@@ -407,7 +488,12 @@ hipError_t launch_kv_compact(const CompactArgs& a, int dim, int layers, hipStrea
 }
 
 hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t st) {
-  k_kv_fork<<<1, kForkThreads, 0, st>>>(a);
+  int lanes = 1;
+  while (lanes < 64 && lanes < a.max_pages) lanes *= 2;
+  if (a.num_pages <= kForkPages && a.seqs <= kForkRows && a.outs <= kForkRows)
+    k_kv_fork<true><<<1, kForkThreads, 0, st>>>(a, lanes);
+  else
+    k_kv_fork<false><<<1, kForkThreads, 0, st>>>(a, lanes);
   return hipGetLastError();
 }
 

@@ -99,15 +99,16 @@ struct AppendPlan {
   int seqs, span;    // span: heads of a thread of the queries' workgroups
   int64_t kv_blocks(int n) const { return token_blocks > 0 ? n * token_blocks : n * reach * groups; }
 };
-// items: (head, K or V) pairs of a workgroup; units: 8-feature units of a query head (0: no queries)
+// items: (head, K or V) pairs of a workgroup; units: threads of a query head (0: no queries); wide: features
+// of a thread where one new token each is expected; groups: given instead of items
 inline AppendPlan append_plan(int seqs, int64_t max_q, int64_t max_pages, int page, int kv_heads, int dim, int heads,
-                              int units, int items, int threads) {
+                              int units, int items, int threads, int groups = 0, int wide = 8) {
   AppendPlan p;
   const int64_t most = kMaxThreads / threads;
-  p.groups = (2 * kv_heads + items - 1) / items;
+  p.groups = groups > 0 ? groups : (2 * kv_heads + items - 1) / items;
   // one new token each: lanes by head and features instead of patches, of which it would fill one lane
   // in page / 8
-  p.token_blocks = max_q == 1 ? ((int64_t)2 * kv_heads * (dim / 8) + threads - 1) / threads : 0;
+  p.token_blocks = max_q == 1 ? ((int64_t)2 * kv_heads * (dim / wide) + threads - 1) / threads : 0;
   const int64_t each = p.token_blocks > 0 ? p.token_blocks : p.groups;
   p.seqs = seqs <= most / each ? seqs : (int)(most / each);
   p.reach = (max_q + page - 2) / page + 1;           // pages that max_q tokens can lie in
