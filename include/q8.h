@@ -479,7 +479,7 @@ size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t 
  * mask: uint64 [T, mask_words] in device memory, 8-byte aligned; mask_words
  * from 1 to 32768.  Everything else, a query that sees no key among it, is as
  * q8_attention_kv8 has it.
- * workspace: q8_attention_workspace_bytes(...) with the same sizes.
+ * workspace: q8_attention_tree_workspace_bytes(...) with the same sizes.
  */
 q8_status q8_attention_kv8_tree(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T,
                                 int64_t Hq, int64_t Hkv, int64_t D, const int32_t* q_start,
@@ -491,6 +491,10 @@ q8_status q8_attention_kv8_tree(const void* q, int64_t q_stride, q8_dtype dtype,
                                 const int32_t* token_positions, float scale, int64_t window,
                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
                                 void* stream);
+
+/* Bytes of workspace q8_attention_kv8_tree needs at these sizes; 0 for invalid ones. */
+size_t q8_attention_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S,
+                                         int64_t max_q, int64_t max_kv, int64_t window);
 
 /*
  * Calls over the caches of all layers, which share one block table: k_cache,

@@ -346,7 +346,7 @@ def test_other_stream_and_graph():
     cos, sin = (up(a) for a in tables_of_angles(2100, 128))
     w = torch.rand(128, device=DEV) + 0.5
     _, batch = batch_of(news, lens, table, 9, 2100)
-    need = q8.q8_attention_workspace_bytes(14, 8, 2, 128, 2, 9, 2100)
+    need = q8.q8_attention_tree_workspace_bytes(14, 8, 2, 128, 2, 9, 2100)
     ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
 
     def step(xin, cache, out):

@@ -2,6 +2,7 @@
 any device work (fake pointers, never dereferenced), and their plain forms."""
 import ctypes
 import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -85,8 +86,9 @@ def test_tree_arguments_and_workspace():
         assert attend(**kw) == 5, kw
     assert attend(mask=None) == 1 and attend(mask=MIS) == 6
     many = dict(T=40, Hq=32, qs=4096, Hkv=8, mq=20, mkv=120000, mp=4000)
-    need = E.lib().q8_attention_workspace_bytes(40, 32, 8, 128, 2, 20, 120000, 0)
+    need = E.lib().q8_attention_tree_workspace_bytes(40, 32, 8, 128, 2, 20, 120000, 0)
     assert need > 0
+    assert E.lib().q8_attention_tree_workspace_bytes(40, 31, 8, 128, 2, 20, 120000, 0) == 0
     assert attend(**many, ws=None) == 7 and attend(**many, wsn=need - 1) == 7 and attend(**many, ws=MIS) == 6
 
 
@@ -176,3 +178,20 @@ def test_plain_compact_and_fork():
     assert out.tolist() == [[5, 3, -1], [5, 0, -1], [7, 1, -1], [-1, -1, -1], [5, 2, -1]]
     assert count.tolist() == [1, 1, 1, 1, 0, 3, 0, 1, 0, 0, 0, 0]
     assert all(np.array_equal(cache[n][0], cache[n][3]) and np.array_equal(cache[n][2], cache[n][3]) for n in cache)
+
+
+def test_every_launch_is_within_its_limits(tmp_path):
+    here = os.path.dirname(os.path.abspath(__file__))
+    csrc = os.path.join(os.path.dirname(here), "w8a8_quantized_linear_channel_amd", "csrc")
+    exe = str(tmp_path / "tree_plan_check")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", f"-I{csrc}",
+                    os.path.join(here, "native", "tree_plan_check.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+@needs_lib
+def test_rows_past_32_bits_are_refused():
+    for T, Hq, want in ((1 << 26, 32, 2), (1 << 30, 2, 2), ((1 << 26) - 64, 32, 5)):
+        assert attend(T=T, Hq=Hq, Hkv=1, D=64, qs=Hq * 64, window=-1) == want, (T, Hq)
+        assert (E.lib().q8_attention_tree_workspace_bytes(T, Hq, 1, 64, 1, 1, 100000, 0) == 0) == (want == 2)

@@ -59,6 +59,7 @@ SIGNATURES = {
                           _P, _P, _P, _SZ, _P]),
     "q8_kv_fork_workspace_bytes": (_SZ, [_I64] * 3),
     "q8_attention_workspace_bytes": (_SZ, [_I64] * 8),
+    "q8_attention_tree_workspace_bytes": (_SZ, [_I64] * 8),
     "q8_quantize_weight_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
     "q8_quantize_act_block": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
     "q8_gemm_fp8_block": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _INT, _P]),

@@ -257,7 +257,7 @@ PyObject* attention_kv8_tree(PyObject* const* a) {
     return not_ours();
   c10::DeviceGuard guard(q->device());
   at::Tensor y = out ? *out : at::empty({T, heads, kv.dim}, q->options()), ws;
-  const size_t need = q8_attention_workspace_bytes(T, heads, kv.heads, kv.dim, kv.seqs, kv.max_q, kv.max_kv, window);
+  const size_t need = q8_attention_tree_workspace_bytes(T, heads, kv.heads, kv.dim, kv.seqs, kv.max_q, kv.max_kv, window);
   if (need) ws = at::empty({(int64_t)need}, kv.table->options().dtype(at::kByte));
   void* st;
   if (!stream_of(dev, &st)) return nullptr;

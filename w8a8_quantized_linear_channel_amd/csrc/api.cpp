@@ -201,14 +201,15 @@ q8::KvView kv_view(const uint8_t* k, const uint8_t* ke, const uint8_t* v, const 
 
 // Splits' partial sums: float [splits, T, Hq, D] and their (maximum, sum) pairs.
 struct AttnWs { size_t part, ml, total; };
-AttnWs attn_ws(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q, int64_t max_kv, int64_t window) {
+AttnWs attn_ws(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q, int64_t max_kv, int64_t window,
+               bool tree = false) {
   AttnWs w{0, 0, 0};
   if (T == 0) return w;
-  const int64_t splits = q8::attn_splits((int)Hq, (int)Hkv, (int)D, (int)S, max_q, max_kv, (int)window);
+  const int64_t splits = (tree ? q8::tree_splits : q8::attn_splits)((int)Hq, (int)Hkv, (int)D, (int)S, max_q, max_kv, (int)window);
   if (splits <= 1) return w;
   Carve c;
   w.part = c.take((size_t)splits * T * Hq * D * 4);
-  w.ml = c.take((size_t)splits * T * Hq * 8);
+  w.ml = c.take((size_t)splits * T * Hq * (tree ? 12 : 8));
   w.total = c.off;
   return w;
 }
@@ -754,13 +755,26 @@ q8_status q8_kv_append_norm(const void* q, int64_t q_stride, const void* k, int6
                 page, q_out, stream);
 }
 
-size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q,
-                                    int64_t max_kv, int64_t window) {
+namespace {
+
+size_t attention_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q, int64_t max_kv,
+                       int64_t window, bool tree) {
   if (check_kv(T, Hkv, D, S, 1, max_q, 1, 32) != Q8_OK || !valid_heads(T, Hq, Hkv) || max_kv < 0 ||
       max_kv > kMaxRows || window < 0)
     return 0;
   window = window > kMaxTokens ? 0 : window;
-  return attn_ws(T, Hq, Hkv, D, S, bound_of(max_q, T), bound_of(max_kv, kMaxRows), window).total;
+  return attn_ws(T, Hq, Hkv, D, S, bound_of(max_q, T), bound_of(max_kv, kMaxRows), window, tree).total;
+}
+
+}  // namespace
+
+size_t q8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q,
+                                    int64_t max_kv, int64_t window) {
+  return attention_bytes(T, Hq, Hkv, D, S, max_q, max_kv, window, false);
+}
+size_t q8_attention_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t S, int64_t max_q,
+                                         int64_t max_kv, int64_t window) {
+  return attention_bytes(T, Hq, Hkv, D, S, max_q, max_kv, window, true);
 }
 
 namespace {
@@ -788,7 +802,7 @@ q8_status attention(const void* q, int64_t q_stride, q8_dtype dtype, int64_t T, 
   if (!std::isfinite(scale) || window < 0) return Q8_ERR_BAD_ARG;
   window = window > kMaxTokens ? 0 : window;           // wider than any sequence: no window
   const int64_t mq = bound_of(max_q, T), mkv = bound_of(max_kv, kMaxRows);
-  const AttnWs ws = attn_ws(T, Hq, Hkv, D, S, mq, mkv, window);
+  const AttnWs ws = attn_ws(T, Hq, Hkv, D, S, mq, mkv, window, tree != nullptr);
   if (ws.total > 0 && (!workspace || workspace_bytes < ws.total)) return Q8_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || (lse && !aligned4(lse)) ||
       (ws.total > 0 && !aligned16(workspace)) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) ||

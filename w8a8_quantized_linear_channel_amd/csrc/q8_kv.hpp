@@ -49,7 +49,7 @@ struct AttnArgs {
   int max_q;
   int64_t max_kv;
   float scale_log2;                // softmax scale times log2(e)
-  float *part, *part_ml;           // [splits, tokens * heads, dim], [splits, tokens * heads, 2]
+  float *part, *part_ml;           // [splits, tokens * heads, dim], [splits, tokens * heads, 2] (trees: 3)
   const uint64_t* mask;            // drafted trees: [tokens, words]
   int words;
   const int32_t* pos;              // [tokens] or null
@@ -57,6 +57,7 @@ struct AttnArgs {
 // Splits of the key axis for this shape (1: no workspace, one launch).
 int attn_splits(int heads, int kv_heads, int dim, int seqs, int64_t max_q, int64_t max_kv, int window);
 hipError_t launch_attention(const AttnArgs& a, int dt, int dim, hipStream_t st);
+int tree_splits(int heads, int kv_heads, int dim, int seqs, int64_t max_q, int64_t max_kv, int window);
 hipError_t launch_attention_tree(const AttnArgs& a, int dt, int dim, hipStream_t st);
 
 // One layer's cache, as a KvView has it.

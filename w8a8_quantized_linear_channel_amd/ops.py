@@ -680,6 +680,11 @@ def q8_attention_kv8(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Opt
     return (y, le) if lse else y
 
 
+def q8_attention_tree_workspace_bytes(T: int, heads: int, kv_heads: int, dim: int, seqs: int, max_q: int, max_kv: int,
+                                      window: int = 0) -> int:
+    return int(_lib.lib().q8_attention_tree_workspace_bytes(T, heads, kv_heads, dim, seqs, max_q, max_kv, window))
+
+
 def q8_attention_kv8_tree(q: torch.Tensor, cache: KvCache, batch: KvBatch, mask: torch.Tensor,
                           positions: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
                           lse: bool = False, out: Optional[torch.Tensor] = None,
@@ -711,7 +716,7 @@ def q8_attention_kv8_tree(q: torch.Tensor, cache: KvCache, batch: KvBatch, mask:
     L = _lib.lib()
     ws, wsn = workspace, 0
     if ws is None:
-        wsn = L.q8_attention_workspace_bytes(T, Hq, Hkv, D, S, batch.max_q, batch.max_kv, window)
+        wsn = L.q8_attention_tree_workspace_bytes(T, Hq, Hkv, D, S, batch.max_q, batch.max_kv, window)
         if wsn:
             ws = torch.empty(wsn, dtype=torch.uint8, device=dev)
     else:
