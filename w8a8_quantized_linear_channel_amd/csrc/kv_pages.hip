@@ -57,12 +57,13 @@ __device__ __forceinline__ int wave_max_i(int v) {
 
 // The kept path of a sequence as far as it is one: entries i, keep[i] from i on, growing, below n.  Returns
 // their number; `stay` receives how many are in place at its front.
-__device__ __forceinline__ int path_of(const int32_t* keep, int most, int n, int lane, int* stay) {
+__device__ __forceinline__ int path_of(const int32_t* keep, int width, int most, int n, int lane, int* stay) {
   int total = 0, still = 0;
   for (int base = 0;; base += 64) {
     const int i = base + lane;
+    // (read before the count is known)
+    const int k = i < width ? keep[i] : -1, before = i > 0 && i < width ? keep[i - 1] : -1;
     const bool in = i < most;
-    const int k = in ? keep[i] : -1, before = in && i > 0 ? keep[i - 1] : -1;
     const uint64_t ok = __ballot(in && k >= i && k < n && k > before), same = __ballot(in && k == i);
     const int run = ok == ~0ull ? 64 : __builtin_ctzll(~ok);
     const uint64_t mine = run == 64 ? ~0ull : ((uint64_t)1 << run) - 1, off = mine & ~same;
@@ -86,9 +87,9 @@ __device__ __forceinline__ uint32_t rescaled4(uint32_t w, const int* shift) {
 }
 
 // Where a page's tokens come from, token i at lane i % 64 of one of two sets (a page has 128 tokens at
-// most): page x head, -1 without one; place in that page, and its exponent byte << 8.
+// most): page x head, -1 without one; place in that page; its exponent byte.
 struct Sources {
-  int ph[2], at[2];
+  int ph[2], off[2], b[2];
 };
 
 template <int D>
@@ -103,7 +104,7 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
   most = most < 0 ? 0 : (most > a.width ? a.width : most);
   const int32_t* const keep = a.keep + (int64_t)s * a.width;
   int stay;
-  const int kept = path_of(keep, most, n, lane, &stay);
+  const int kept = path_of(keep, a.width, most, n, lane, &stay);
   if (says && lane == 0) a.len_out[s] = past + kept < 0 ? 0 : past + kept;
   const int64_t cap = (int64_t)kv.max_pages * page;
   // the slots that receive a token
@@ -120,7 +121,7 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
   for (; lo < hi; lo = (lo & ~(page - 1)) + page) {
     const int stop = (lo & ~(page - 1)) + page, top = hi < stop ? hi : stop, count = top - lo;
     // the sources of all tokens in one go, a token a lane
-    Sources from{{-1, -1}, {0, 0}};
+    Sources from{{-1, -1}, {0, 0}, {0, 0}};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = 64 * h + lane;
@@ -128,7 +129,8 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
       const int slot = past + keep[lo + i - past], p = page_at(slot);
       if (p < 0) continue;
       from.ph[h] = p * kv.kv_heads + head;
-      from.at[h] = (slot & (page - 1)) | (int)exps[from.ph[h]] << 8;
+      from.off[h] = slot & (page - 1);
+      from.b[h] = exps[from.ph[h]];
     }
     const int to = page_at(lo);
     if (to < 0) continue;
@@ -143,35 +145,47 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
     };
     if (!is_v) {
       // 16 features a lane, G tokens at once; U of those in registers
-      constexpr int C = D / 16, G = 64 / C, U = 4;
+      constexpr int C = D / 16, G = 64 / C, U = 2;
       const int c = lane % C;
       v4i x[U];
-      int at[U];                     // -1: nothing
+      int u_b[U];                    // exponent byte; -1: nothing
       auto load = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int i = i0 + u * G + lane / C;
-          int ph = __shfl(from.ph[0], i & 63);
-          at[u] = __shfl(from.at[0], i & 63);
+          int ph = __shfl(from.ph[0], i & 63), off = __shfl(from.off[0], i & 63);
           if (page > 64) {
-            const int p1 = __shfl(from.ph[1], i & 63), a1 = __shfl(from.at[1], i & 63);
+            const int p1 = __shfl(from.ph[1], i & 63), o1 = __shfl(from.off[1], i & 63);
             ph = i < 64 ? ph : p1;
-            at[u] = i < 64 ? at[u] : a1;
+            off = i < 64 ? off : o1;
           }
-          at[u] = i < count && ph >= 0 ? at[u] : -1;
           x[u] = v4i{0, 0, 0, 0};
-          if (at[u] >= 0) x[u] = *(const v4i*)(codes + ((int64_t)ph * page + (at[u] & 255)) * D + 16 * c);
+          u_b[u] = -1;
+          if (i < count && ph >= 0) {
+            x[u] = *(const v4i*)(codes + ((int64_t)ph * page + off) * D + 16 * c);
+            u_b[u] = 0;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * G + lane / C;
+          int eb = __shfl(from.b[0], i & 63);
+          if (page > 64) {
+            const int e1 = __shfl(from.b[1], i & 63);
+            eb = i < 64 ? eb : e1;
+          }
+          u_b[u] = u_b[u] < 0 ? -1 : eb;
         }
       };
       for (int i0 = 0; i0 < count; i0 += U * G) {
         load(i0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (at[u] < 0) continue;
+          if (u_b[u] < 0) continue;
           int big = 0;
 #pragma unroll
           for (int w = 0; w < 4; ++w) big = largest4((uint32_t)x[u][w], big);
-          const int w = wanted(big, at[u] >> 8);
+          const int w = wanted(big, u_b[u]);
           want = w > want ? w : want;
         }
       }
@@ -189,8 +203,8 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
         if (count > U * G) load(i0);               // (else they are there)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (at[u] < 0) continue;
-          const int shift = (at[u] >> 8) - b;
+          if (u_b[u] < 0) continue;
+          const int shift = u_b[u] - b;
           if (shift != 0)
 #pragma unroll
             for (int w = 0; w < 4; ++w) x[u][w] = (int)rescaled4((uint32_t)x[u][w], shift);
@@ -218,14 +232,21 @@ __device__ void compact_item(const CompactArgs& a, const CacheLayer& layer, int 
             shift[u][e] = -1;
             if (i < 0 || i >= count) continue;
             const int ph = __builtin_amdgcn_readlane(i < 64 ? from.ph[0] : from.ph[1], i & 63);
-            const int at = __builtin_amdgcn_readlane(i < 64 ? from.at[0] : from.at[1], i & 63);
+            const int off = __builtin_amdgcn_readlane(i < 64 ? from.off[0] : from.off[1], i & 63);
             if (ph < 0) continue;
-            shift[u][e] = at >> 8;
-            const uint8_t* const p = codes + (int64_t)ph * page * D + (at & 255);
+            shift[u][e] = 0;
+            const uint8_t* const p = codes + (int64_t)ph * page * D + off;
 #pragma unroll
             for (int j = 0; j < F; ++j) x[u][j] |= (uint32_t)p[(lane + 64 * j) * page] << (8 * e);
           }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = w0 + 4 * (i0 + u) + e - old;
+            if (shift[u][e] == 0) shift[u][e] = __builtin_amdgcn_readlane(i < 64 ? from.b[0] : from.b[1], i & 63);
+          }
       };
       for (int i0 = 0; i0 < words; i0 += U) {
         load(i0);

@@ -92,14 +92,15 @@ inline AttnPlan tree_plan(int64_t rows, int dim, int kv_heads, int seqs, int64_t
   const int64_t pairs = (int64_t)seqs * kv_heads;
   int64_t keys = max_kv;
   if (window > 0 && window + max_q + 2 * kTile < keys) keys = window + max_q + 2 * kTile;
-  // Blocks that share codes where they are two thirds full at least and there is much to do on long keys
-  // (8 kv heads of 128 features, shared against 16 or 32 rows a workgroup: 240 rows on 60000 keys 85 against
-  // 111 us, 600 on 20000 85 against 129, 240 on 8000 35 against 29), or very much (32 sequences of 256 rows
-  // on 4000 125 against 157, of 176 rows 109 against 102; 4 of 732 on 4000 99 against 60).
+  // Blocks that share codes where they are well filled and there is much to do on long keys (8 kv heads of 128
+  // features, shared against 16 or 32 rows a workgroup: 240 rows on 60000 keys 85 against 111 us, 600 on 20000 85
+  // against 129, 2 sequences of 160 on up to 60000 136 against 155, 240 on 8000 35 against 29), or very much (32
+  // sequences of 256 rows on 4000 125 against 157, of 176 rows 109 against 102; 4 of 732 on 4000 99 against 60).
   // Sequences and heads that alone pass a launch of that kernel: the other's grid has them in y and z.
   const int64_t most = dim == 256 ? 128 : 256, whole = (rows + most - 1) / most * most;
   const double work = (double)pairs * (double)rows * (double)keys * dim;
-  const bool many = 3 * rows >= 2 * whole && work >= (keys >= 16384 ? 5.8e9 : 2.4e10) && pairs <= kMaxThreads / 512;
+  const bool full = keys >= 16384 && dim != 64 ? 5 * rows >= 3 * whole : 4 * rows >= 3 * whole;
+  const bool many = full && work >= (keys >= 16384 ? 5.8e9 : 2.4e10) && pairs <= kMaxThreads / 512;
   // 32 rows a wave read and convert the codes half as often, 16 leave more workgroups and more waves: 32 where
   // blocks of 16 would read much (8 kv heads of 128 features: 32 sequences of 64 rows on 4000 keys 51 against
   // 79 us, 8 of 112 on 2000 20.4 against 22.5, of 64 15.8 against 21.7 the other way).  64 features are faster
@@ -110,8 +111,8 @@ inline AttnPlan tree_plan(int64_t rows, int dim, int kv_heads, int seqs, int64_t
   const int64_t groups = pairs * p.blocks;
   // Splits only to give every CU a workgroup (32 sequences of 32 rows on 4000 keys: none 39 us, as many as
   // make 512 workgroups 45, 1024 53), but none longer than 8192 keys with few rows, so that one long sequence
-  // among many does not hold up the rest.  A share under 1024 keys costs the join more than it saves (one sequence of 48 rows on 700
-  // keys 11.2 us whole, 13.2 in two), of 256 features under 512.
+  // among many does not hold up the rest.  A share under 1024 keys costs the join more than it saves (one
+  // sequence of 48 rows on 700 keys 11.2 us whole, 13.2 in two), of 256 features under 512.
   int64_t want = 256 / groups;
   const int64_t least = many ? 256 : dim == 256 ? 512 : 1024;
   if (!many && want < keys / 8192) want = keys / 8192;
