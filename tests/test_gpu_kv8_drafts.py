@@ -88,6 +88,24 @@ def test_append_sizes_of_values():
     run_append(rng, [9, 5], [4, 70], 2, 1, 64, 64, HF, rot=64, angles=50)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_infinite_and_nan_queries(D):
+    """A NaN makes its head NaN; beside an infinity (r = 0) the other features are 0; other heads are as they were."""
+    rng = np.random.default_rng(D)
+    x = torch.from_numpy(rng.standard_normal((9, 6, D)).astype(np.float32)).to(BF)
+    x[0, 1, 3], x[2, 0, D - 1], x[4, 3, 5], x[8, 2, 0] = float("inf"), float("nan"), -float("inf"), float("inf")
+    x[8, 2, 1] = float("nan")
+    w = torch.from_numpy((1 + 0.5 * rng.standard_normal(D)).astype(np.float32))
+    _, batch = batch_of([9], [9], [[0]])
+    k = x[:, 4:].to(DEV)
+    got = q8.q8_kv_append_norm(k[:, :1], k[:, 1:], q8.q8_kv_cache(1, 1, D, page=32, device=DEV), batch, q=x[:, :4].to(DEV),
+                               q_weight=w.to(DEV)).cpu().float()
+    with np.errstate(invalid="ignore"):
+        want = torch.from_numpy(M.normalised(x[:, :4].float().numpy(), w.numpy(), 1e-6)).to(BF).float()
+    assert want[0, 1].isnan().sum() == 1 and want[2, 0].isnan().all() and want[8, 2].isnan().all()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+
+
 def test_append_zeros_and_no_tokens():
     cache = q8.q8_kv_cache(2, 1, 64, page=32, device=DEV)
     _, batch = batch_of([3], [3], [[0]])

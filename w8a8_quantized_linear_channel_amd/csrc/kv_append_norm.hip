@@ -37,11 +37,12 @@ __device__ __forceinline__ double squares8(const float* v, double sum) {
   for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)v[e], (double)v[e], sum);
   return sum;
 }
-// 1 / sqrt(m): the hardware's t (some 23 bits) times (1 - e)^(-1/2) = 1 + e / 2 + 3 e^2 / 8 + ..., e = 1 - m t^2
+// 1 / sqrt(m): the hardware's t (some 23 bits) times (1 - e)^(-1/2) = 1 + e / 2 + 3 e^2 / 8 + ..., e = 1 - m t^2;
+// 0 for an infinite m, where that is NaN
 __device__ __forceinline__ float inverse_root(double m) {
   const double t = __builtin_amdgcn_rsq(m);
   const double e = __builtin_fma(-(m * t), t, 1.0);
-  return (float)__builtin_fma(t * e, __builtin_fma(e, 0.375, 0.5), t);
+  return (float)(m < __builtin_huge_val() ? __builtin_fma(t * e, __builtin_fma(e, 0.375, 0.5), t) : t);
 }
 __device__ __forceinline__ void load_weight(const AppendArgs& a, const void* w, int c, float* v) {
   if (w == nullptr) {
