@@ -52,10 +52,19 @@ struct TreeRows {
       for (int n = 0; n < NT; ++n) acc[r][n] = v4f{0, 0, 0, 0};
     }
   }
+  // The first cached key that each row sees, and its bits of the 16 keys from kb + 16 lg on
+  __device__ __forceinline__ void seen(const AttnArgs& a, const Span& sp, int kb, int lr, int lg, int (&low)[R], uint32_t (&bits)[R]) const {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int tok = token(r, lr), at = a.window > 0 ? drafted_at(a, sp.first, tok, sp.past, sp.n) - a.window + 1 : 0;
+      low[r] = at < sp.past ? at : sp.past;          // (the window is the cached keys' alone)
+      bits[r] = drafted<16>(a.mask + (int64_t)(sp.first + tok) * a.words, a.words, kb + 16 * lg - sp.past);
+    }
+  }
   // Scores sc of the tile at kb (register 4 t + i is key kb + 16 lg + 4 t + i, exponent bytes exps) to the
   // product's weights pf, the sums and the references with them
   __device__ __forceinline__ void weigh(const AttnArgs& a, const Span& sp, const Keys& ks, int kb, int lr, int lg, int exps, float scale,
-                                        v4f (&sc)[R][4], v4i (&pf)[R][2]) {
+                                        const int (&low)[R], const uint32_t (&bits)[R], v4f (&sc)[R][4], v4i (&pf)[R][2]) {
     const int keyv = kb + 16 * lg;
     // not 0: a masked score of -inf stays one
     const float kscale = fmaxf(exp_byte(exps & 255) * scale, 1.17549435e-38f), own_b = (float)(exps >> 8);
@@ -63,16 +72,12 @@ struct TreeRows {
       // register 4 t + i is key keyv + 4 t + i
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int tok = token(r, lr);
-        int low = a.window > 0 ? drafted_at(a, sp.first, tok, sp.past, sp.n) - a.window + 1 : 0;
-        low = low < sp.past ? low : sp.past;         // (the window is the cached keys' alone)
-        const uint32_t bits = drafted<16>(a.mask + (int64_t)(sp.first + tok) * a.words, a.words, keyv - sp.past);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = keyv + 4 * t + i;
-            sc[r][t][i] = key >= low && key < ks.hi && (bits >> (4 * t + i) & 1) ? sc[r][t][i] : -INFINITY;
+            sc[r][t][i] = key >= low[r] && key < ks.hi && (bits[r] >> (4 * t + i) & 1) ? sc[r][t][i] : -INFINITY;
           }
       }
     }
@@ -199,6 +204,14 @@ __device__ __forceinline__ v4i cleared(v4i x, int keyv, const Keys& ks, bool car
   return x;
 }
 
+// A barrier for what is in LDS: loads on their way to registers stay on it
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <int D, int DT, int NW, int R, int EU>
 __global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int row_tiles, int chunk) {
   constexpr int KL = D / 64, NT = D / 16, RB = 16 * R;
@@ -209,6 +222,10 @@ __global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int
   const int split = blockIdx.x, head = blockIdx.y;
   const int s = blockIdx.z / row_tiles, tile0 = blockIdx.z % row_tiles;
   const int group = a.heads / kv.kv_heads;
+  {
+    const int q0 = kv.q_start[s], q1 = kv.q_start[s + 1], len = kv.kv_len[s];
+    asm volatile("" ::"s"(q0), "s"(q1), "s"(len));             // all requested at once
+  }
   const Span sp = span_of(a, s);
   const int rows = sp.n * group;
   const bool split_out = gridDim.x > 1;
@@ -241,34 +258,23 @@ __global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int
     constexpr int kStride = NW * kTile, kRun = kMeta / 2 * kTile;
     for (int run = kb0; run < kb1; run += kRun) {
     const int stop = run + (int64_t)kRun < kb1 ? run + kRun : kb1;
-    __syncthreads();                 // the run before is read
-    for (int i = tid; i < kMeta; i += 64 * NW) {
-      // a half that no row sees reads page 0
-      const int key = run + 32 * i;
-      const bool seen = key < khi && key + 32 > klo;
-      int p = seen ? kv.table[(int64_t)s * kv.max_pages + (key >> page_log2)] : 0;
-      p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
-      p = p * kv.kv_heads + head;
-      s_ph[i] = p;
-      s_exp[i] = kv.ke[p] | kv.ve[p] << 8;
-    }
-    __syncthreads();
     v4i kx[4][KL], vx[NT];
-    auto request_keys = [&](int kb) {
+    // ph: page x head of the 32-key half that the lane reads
+    auto request_keys = [&](int kb, auto ph) {
       int me = lane;
       asm volatile("" : "+v"(me));                 // (what follows from it need not live through the loop)
-      const int row = me & 15, half = ((kb - run) >> 5) + (row >> 3), off = (kb + 16 * (row >> 2)) & (kv.page - 1);
-      const uint8_t* const p = kv.k + ((int64_t)s_ph[half] * kv.page + (off + (row & 3))) * D + 16 * (me >> 4);
+      const int row = me & 15, off = (kb + 16 * (row >> 2)) & (kv.page - 1);
+      const uint8_t* const p = kv.k + ((int64_t)ph(row >> 3) * kv.page + (off + (row & 3))) * D + 16 * (me >> 4);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < KL; ++i) kx[t][i] = *(const v4i*)(p + t * 4 * D + 64 * i);
     };
-    auto request_values = [&](int kb) {
+    auto request_values = [&](int kb, auto ph) {
       int me = lane;
       asm volatile("" : "+v"(me));
-      const int g = me >> 4, half = ((kb - run) >> 5) + (g >> 1), off = (kb + 16 * g) & (kv.page - 1);
-      const uint8_t* const p = kv.v + ((int64_t)s_ph[half] * D + (me & 15)) * kv.page + off;
+      const int g = me >> 4, off = (kb + 16 * g) & (kv.page - 1);
+      const uint8_t* const p = kv.v + ((int64_t)ph(g >> 1) * D + (me & 15)) * kv.page + off;
 #pragma unroll
       for (int n = 0; n < NT; ++n) vx[n] = *(const v4i*)(p + 16 * n * kv.page);
     };
@@ -276,12 +282,44 @@ __global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int
     // Every tile requests the next one, the last one itself again: with a request that may be left out the
     // compiler cannot count the loads in flight, and waits for all of them.
     int kb = run + wave * kTile;
-    if (kb < stop) {
-      request_keys(kb);
-      request_values(kb);
+    // Page x head of the half at `key`; one that no row sees reads page 0
+    auto ph_of = [&](int key) {
+      const bool seen = key < khi && key + 32 > klo;
+      int p = seen ? kv.table[(int64_t)s * kv.max_pages + (key >> page_log2)] : 0;
+      p = p < 0 ? 0 : (p >= kv.num_pages ? kv.num_pages - 1 : p);
+      return p * kv.kv_heads + head;
+    };
+    // The first tiles are requested as soon as their pages are known, beside the run's exponents
+    {
+      constexpr int kEach = kMeta / (64 * NW);
+      static_assert(kMeta % (64 * NW) == 0, "entries of a thread");
+      int ph[kEach], eb[kEach];
+      const int pa = ph_of(kb), pb = ph_of(kb + 32);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) ph[i] = ph_of(run + 32 * (tid + 64 * NW * i));
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) eb[i] = kv.ke[ph[i]] | kv.ve[ph[i]] << 8;
+      auto mine = [&](int half) { return half ? pb : pa; };
+      request_keys(kb, mine);        // (a wave without a tile some others: with a branch all wait for it)
+      request_values(kb, mine);
+      lds_barrier();                 // the run before is read
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        s_ph[tid + 64 * NW * i] = ph[i];
+        s_exp[tid + 64 * NW * i] = eb[i];
+      }
+      lds_barrier();
     }
     for (; kb < stop; kb += kStride) {
       const int keyv = kb + 16 * lg, exps = s_exp[((kb - run) >> 5) + (lg >> 1)];
+      // (requested ahead of the keys behind this tile)
+      int low[R];
+      uint32_t bits[R];
+      if (!(kb >= all_lo && kb + kTile <= all_hi)) {
+        int me = lane;
+        asm volatile("" : "+v"(me));
+        x.seen(a, sp, kb, me & 15, me >> 4, low, bits);
+      }
       v4f sc[R][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -299,12 +337,13 @@ __global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int
       }
       __builtin_amdgcn_sched_barrier(0);
       const int next = kb + kStride < stop ? kb + kStride : kb;
-      request_keys(next);
+      auto listed = [&](int half) { return s_ph[((next - run) >> 5) + half]; };
+      request_keys(next, listed);
       __builtin_amdgcn_sched_barrier(0);
       v4i pf[R][2];
       int at_lane = lane;
       asm volatile("" : "+v"(at_lane));             // (what follows from it need not live through the loop)
-      x.weigh(a, sp, ks, kb, at_lane & 15, at_lane >> 4, exps, scale, sc, pf);
+      x.weigh(a, sp, ks, kb, at_lane & 15, at_lane >> 4, exps, scale, low, bits, sc, pf);
       if (__builtin_expect(careful || kb < klo || kb + kTile > khi, 0)) {
         int at = keyv;
         asm volatile("" : "+v"(at));               // nothing of this ahead of the loop
@@ -324,7 +363,7 @@ __global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      request_values(next);
+      request_values(next, listed);
       __builtin_amdgcn_sched_barrier(0);
     }
     }
