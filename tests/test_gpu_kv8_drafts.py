@@ -270,6 +270,21 @@ def test_tree_long_keys_are_split_and_joined():
     run_tree(np.random.default_rng(4), [30], [6000], 4, 1, 256, 64, BF, window=3000)
 
 
+@pytest.mark.parametrize("D,dt", [(64, HF), (128, BF), (256, BF)])
+@pytest.mark.parametrize("S", [2, 40, 64, 65])
+def test_tree_many_sequences(S, D, dt):
+    """Batches whose workgroups follow each other, taken by length: lengths that are alike, empty sequences among
+    them, up to 64 (one a lane) and more; bounds that ask for 16 rows a wave and for 32."""
+    rng = np.random.default_rng(S)
+    lens = rng.choice([0, 1, 33, 90, 90, 90, 150, 200], S)
+    news = np.minimum(lens, rng.integers(0, 10, S))
+    news[0], lens[0] = 9, 120
+    for most in (None, 5000):
+        for _ in range(2 if S == 2 else 1):
+            run_tree(rng, news.tolist(), lens.tolist(), 32, 8, D, 32, dt, max_q=300 if S == 2 else None, max_kv=most)
+    run_tree(rng, [3] * S, [40] * S, 32, 8, D, 32, dt, max_q=300 if S == 2 else 9)
+
+
 def test_tree_bounds_that_are_too_small_and_scales():
     rng = np.random.default_rng(8)
     run_tree(rng, [70, 3], [600, 2000], 4, 2, 64, 64, BF, max_q=1, max_kv=1)

@@ -13,6 +13,12 @@
 // and two waves fit a SIMD: one's conversions and exponentials run beside the other's
 // MFMAs.  The running maximum is a reference that is only moved when a score passes
 // it by 8, as in k_attn_tiles.
+//
+// 32 users' drafts on 700 to 4100 keys (88 rows, 8 kv heads, 137 MB of codes): 65 us, in which VALU
+// instructions take a good third of each SIMD's cycles and MFMAs a seventh.  Codes that each wave's own DMA puts into
+// LDS took as long as these loads, for all that a load of 16 rows looks up 64 lines (72 us both, then); one workgroup of 8
+// waves a CU instead of two of 4 took 82: what is left is where a workgroup starts and ends, lengths, pages, codes and
+// masks one after another, and the turns of a SIMD's two waves.
 #include "q8_attn.hpp"
 
 namespace q8 {
@@ -213,15 +219,27 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 template <int D, int DT, int NW, int R, int EU>
-__global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int row_tiles, int chunk) {
+__global__ __launch_bounds__(64 * NW, EU) void k_tree_rows(const AttnArgs a, int row_tiles, int chunk, int sorted) {
   constexpr int KL = D / 64, NT = D / 16, RB = 16 * R;
   const KvView& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int split = blockIdx.x, head = blockIdx.y;
-  const int s = blockIdx.z / row_tiles, tile0 = blockIdx.z % row_tiles;
+  int s = blockIdx.z / row_tiles;
+  const int tile0 = blockIdx.z % row_tiles;
   const int group = a.heads / kv.kv_heads;
+  if (sorted) {
+    // the s-th longest, so that the workgroups that start last are short ones: lane l counts the sequences
+    // that go before l
+    const int len = lane < kv.seqs ? kv.kv_len[lane] : -1;
+    int before = 0;
+    for (int i = 0; i < kv.seqs; ++i) {
+      const int other = __builtin_amdgcn_readlane(len, i);
+      before += other > len || (other == len && i < lane) ? 1 : 0;
+    }
+    s = __builtin_ctzll(__ballot(lane < kv.seqs && before == s));
+  }
   {
     const int q0 = kv.q_start[s], q1 = kv.q_start[s + 1], len = kv.kv_len[s];
     asm volatile("" ::"s"(q0), "s"(q1), "s"(len));             // all requested at once
@@ -449,11 +467,16 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t st) {
   const AttnPlan p = tree_plan(rows, D, a.kv.kv_heads, a.kv.seqs, a.max_q, a.max_kv, a.window);
   const int blocks = (int)p.blocks;
   if (p.per <= 32) {
+    // The longest sequences first where one to four rounds of workgroups follow each other (32 sequences on 700
+    // to 4100 keys, 8 kv heads of 128 features: 88 rows 72.4 -> 65.5 us, 176 rows 97 -> 91); more rounds
+    // even themselves out (64 features, 176 rows, six rounds: 62.4 -> 64.9).
+    const int64_t groups = (int64_t)p.splits * a.kv.kv_heads * p.blocks * a.kv.seqs;
+    const int sorted = a.kv.seqs > 1 && a.kv.seqs <= 64 && a.window == 0 && groups > 512 && groups <= 2048;
     const dim3 grid((unsigned)p.splits, (unsigned)a.kv.kv_heads, (unsigned)(p.blocks * a.kv.seqs));
     if constexpr (D == 128) {
-      if (p.per == 32) k_tree_rows<D, DT, 4, 2, 2><<<grid, 256, 0, st>>>(a, blocks, p.chunk);
+      if (p.per == 32) k_tree_rows<D, DT, 4, 2, 2><<<grid, 256, 0, st>>>(a, blocks, p.chunk, sorted);
     }
-    if (p.per == 16) k_tree_rows<D, DT, 4, 1, D == 256 ? 1 : 2><<<grid, 256, 0, st>>>(a, blocks, p.chunk);
+    if (p.per == 16) k_tree_rows<D, DT, 4, 1, D == 256 ? 1 : 2><<<grid, 256, 0, st>>>(a, blocks, p.chunk, sorted);
   } else {
     const unsigned grid = (unsigned)(p.blocks * a.kv.seqs * a.kv.kv_heads * p.splits);
     if constexpr (D == 256) k_attn_tiles<D, DT, 4, true><<<grid, 256, 0, st>>>(a, blocks, p.splits, p.chunk);
