@@ -7,6 +7,12 @@
 // a partner's feature is in the same thread, and the finished values wait in
 // registers for the page's maximum.  A thread of the values takes 8 tokens x 8
 // features, kept as they were read.  Everything is read once.
+//
+// 15372 new tokens of 6 prompts (32 query and 8 kv heads of 128 features, f16, pages of 128, 64 features turned as
+// neighbours): 97 us, 350 MB at 3.6 TB/s where a large copy moves 5.2.  Keys and values alone take 45 (a page's codes
+// wait for its largest value), queries alone at the copy's rate would take 44.  A head's groups of 8 lie beside
+// each other over the threads (u and u + dim / 16): 16-byte requests of neighbouring lanes fill whole lines (102 us with 32
+// bytes a thread in a row).  12 drafts or 128 single tokens: 6 us, a chain of length, page, exponent and codes.
 #include "q8_kv_append.hpp"
 
 namespace q8 {
@@ -61,25 +67,27 @@ __device__ __forceinline__ int turned_by(const AppendArgs& a, int token, int slo
   const int p = a.pos ? a.pos[token] : slot;
   return p < 0 ? 0 : p;
 }
-// The two groups of 8 features of thread u of a head, and whether they are turned.
+// The two groups of 8 features of thread u of a head, and whether they are turned: where the rotation leaves
+// the choice, neighbouring threads have neighbouring groups.
 struct Groups {
   int c0, c1;
-  bool turned;
+  bool t0, t1;
 };
+template <int D>
 __device__ __forceinline__ Groups groups_of(const AppendArgs& a, int u) {
-  Groups g;
   const int pairs = a.rot >> 4;
-  g.turned = u < pairs;
-  g.c0 = a.interleaved ? 2 * u : (g.turned ? u : 2 * u);
-  g.c1 = !a.interleaved && g.turned ? u + pairs : g.c0 + 1;
-  return g;
+  if (a.interleaved || a.rot == 0) return Groups{u, u + D / 16, u < 2 * pairs, u + D / 16 < 2 * pairs};
+  return u < pairs ? Groups{u, u + pairs, true, true} : Groups{2 * u, 2 * u + 1, false, false};
 }
-// Their cosines and sines at a position: those of pairs 8u .. 8u+7 either way (pairs (2 i, 2 i + 1): the
-// first four are the first group's).  Threads whose features are not turned read others' and leave them.
+// Their cosines and sines at a position, of four pairs each where pairs are neighbours (2 i, 2 i + 1), else
+// those of pairs 8u .. 8u+7.  Threads whose features are not turned read others' and leave them.
 __device__ __forceinline__ void load_angles(const AppendArgs& a, const Groups& g, int u, int pos, float* co, float* si) {
-  const int64_t at = (int64_t)(pos < a.positions ? pos : a.positions - 1) * (a.rot >> 1) + (g.turned ? 8 * u : 0);
-  load8<DT_F32>(a.cos, at, co);
-  load8<DT_F32>(a.sin, at, si);
+  const int64_t row = (int64_t)(pos < a.positions ? pos : a.positions - 1) * (a.rot >> 1);
+  const int o0 = g.t0 ? (a.interleaved ? 4 * g.c0 : 8 * u) : 0, o1 = a.interleaved ? (g.t1 ? 4 * g.c1 : 0) : o0 + 4;
+  *(v4f*)co = *(const v4f*)(a.cos + row + o0);
+  *(v4f*)(co + 4) = *(const v4f*)(a.cos + row + o1);
+  *(v4f*)si = *(const v4f*)(a.sin + row + o0);
+  *(v4f*)(si + 4) = *(const v4f*)(a.sin + row + o1);
 }
 // A head's 16 features of this thread normalised (weights given) and turned
 template <int D>
@@ -93,17 +101,23 @@ __device__ __forceinline__ void finish16(const AppendArgs& a, const Groups& g, b
       w[e] = w[e] * r * w1[e];
     }
   }
-  if (a.rot == 0 || !g.turned) return;
+  if (a.rot == 0 || !g.t0) return;                 // (the second group is turned only where the first is)
   {
 #pragma clang fp contract(off)
     if (a.interleaved) {                                     // uniform
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float p = v[2 * i], q = v[2 * i + 1], r = w[2 * i], s = w[2 * i + 1];
+        const float p = v[2 * i], q = v[2 * i + 1];
         v[2 * i] = p * co[i] - q * si[i];
         v[2 * i + 1] = q * co[i] + p * si[i];
-        w[2 * i] = r * co[4 + i] - s * si[4 + i];
-        w[2 * i + 1] = s * co[4 + i] + r * si[4 + i];
+      }
+      if (g.t1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float r = w[2 * i], s = w[2 * i + 1];
+          w[2 * i] = r * co[4 + i] - s * si[4 + i];
+          w[2 * i + 1] = s * co[4 + i] + r * si[4 + i];
+        }
       }
     } else {
 #pragma unroll
@@ -180,7 +194,7 @@ __device__ __forceinline__ void append_keys(const AppendArgs& a, int s, int j0, 
   const int head = group * SH::kKeyItems + wave / WAVES;
   const bool have = head < kv.kv_heads && in_item < SH::kKeys;
   const int u = in_item % U, tg = in_item / U;
-  const Groups g = groups_of(a, u);
+  const Groups g = groups_of<D>(a, u);
   float w0[8], w1[8];
   load_weight(a, a.kw, g.c0, w0);
   load_weight(a, a.kw, g.c1, w1);
@@ -359,7 +373,7 @@ __device__ __forceinline__ void append_head(const AppendArgs& a, int s, int firs
   const int64_t ph = (int64_t)(here ? page : 0) * kv.kv_heads + head;
   uint8_t* const exps = (V ? kv.ve : kv.ke) + ph;
   const int had = *exps;
-  const Groups g = V ? Groups{2 * u, 2 * u + 1, false} : groups_of(a, u);
+  const Groups g = V ? Groups{u, u + U, false, false} : groups_of<D>(a, u);
   const void* const x = V ? a.v : a.k;
   const int64_t from = (int64_t)first * (V ? a.v_stride : a.k_stride) + (int64_t)head * D;
   float v[8], w[8];
@@ -432,7 +446,7 @@ __device__ __forceinline__ void norm_queries(const AppendArgs& a, int s, int blo
   const int spans = (a.heads + span - 1) / span, per = U * spans;
   const int64_t all = (int64_t)(end - first) * per;
   const int u = threadIdx.x % U;                             // (blocks of threads are whole heads)
-  const Groups g = groups_of(a, u);
+  const Groups g = groups_of<D>(a, u);
   float w0[8], w1[8];
   load_weight(a, a.qw, g.c0, w0);
   load_weight(a, a.qw, g.c1, w1);
