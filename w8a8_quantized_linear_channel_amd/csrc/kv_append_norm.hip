@@ -156,6 +156,13 @@ __device__ __forceinline__ float item_max(float v, float* red) {
   return v;
 }
 
+// A lane's place, so that what follows from it is computed in the loop (over pages, of which there is one as a
+// rule) and not kept in registers ahead of it
+__device__ __forceinline__ int in_loop(int place) {
+  asm volatile("" : "+v"(place));
+  return place;
+}
+
 // The slots of a sequence's new tokens
 struct Slots {
   int first, past, lo, hi;
@@ -190,16 +197,17 @@ __device__ __forceinline__ void append_keys(const AppendArgs& a, int s, int j0, 
   const KvView& kv = a.kv;
   const Slots sl = slots_of<B>(kv, s);
   if (sl.lo >= sl.hi) return;
-  const int wave = threadIdx.x >> 6, in_item = (wave % WAVES) * 64 + (threadIdx.x & 63);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int head = group * SH::kKeyItems + wave / WAVES;
-  const bool have = head < kv.kv_heads && in_item < SH::kKeys;
-  const int u = in_item % U, tg = in_item / U;
-  const Groups g = groups_of<D>(a, u);
-  float w0[8], w1[8];
-  load_weight(a, a.kw, g.c0, w0);
-  load_weight(a, a.kw, g.c1, w1);
   const int last = (sl.hi - 1) / B;
   for (int lp = sl.lo / B + j0; lp <= last; lp += a.reach) {
+    const int in_item = in_loop((wave % WAVES) * 64 + (threadIdx.x & 63));
+    const bool have = head < kv.kv_heads && in_item < SH::kKeys;
+    const int u = in_item % U, tg = in_item / U;
+    const Groups g = groups_of<D>(a, u);
+    float w0[8], w1[8];
+    load_weight(a, a.kw, g.c0, w0);
+    load_weight(a, a.kw, g.c1, w1);
     const int page = kv.table[(int64_t)s * kv.max_pages + lp];
     const bool here = page >= 0 && page < kv.num_pages;
     const int64_t ph = (int64_t)(here ? page : 0) * kv.kv_heads + (have ? head : 0);
@@ -262,12 +270,13 @@ __device__ __forceinline__ void append_values(const AppendArgs& a, int s, int j0
   const KvView& kv = a.kv;
   const Slots sl = slots_of<B>(kv, s);
   if (sl.lo >= sl.hi) return;
-  const int wave = threadIdx.x >> 6, in_item = (wave % WAVES) * 64 + (threadIdx.x & 63);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int head = group * SH::kValItems + wave / WAVES;
-  const bool have = head < kv.kv_heads && in_item < SH::kVals;
-  const int c = in_item % C, tg = in_item / C;
   const int last = (sl.hi - 1) / B;
   for (int lp = sl.lo / B + j0; lp <= last; lp += a.reach) {
+    const int in_item = in_loop((wave % WAVES) * 64 + (threadIdx.x & 63));
+    const bool have = head < kv.kv_heads && in_item < SH::kVals;
+    const int c = in_item % C, tg = in_item / C;
     const int page = kv.table[(int64_t)s * kv.max_pages + lp];
     const bool here = page >= 0 && page < kv.num_pages;
     const int64_t ph = (int64_t)(here ? page : 0) * kv.kv_heads + (have ? head : 0);
