@@ -9,10 +9,11 @@
 // features, kept as they were read.  Everything is read once.
 //
 // 15372 new tokens of 6 prompts (32 query and 8 kv heads of 128 features, f16, pages of 128, 64 features turned as
-// neighbours): 97 us, 350 MB at 3.6 TB/s where a large copy moves 5.2.  Keys and values alone take 45 (a page's codes
-// wait for its largest value), queries alone at the copy's rate would take 44.  A head's groups of 8 lie beside
-// each other over the threads (u and u + dim / 16): 16-byte requests of neighbouring lanes fill whole lines (102 us with 32
-// bytes a thread in a row).  12 drafts or 128 single tokens: 6 us, a chain of length, page, exponent and codes.
+// neighbours): 82 us, 350 MB at 4.3 TB/s where a large copy moves 5.2.  Keys and values alone take 29, queries alone at
+// the copy's rate would take 44.  A head's groups of 8 lie beside each other over the threads (u and u + dim / 16), so
+// that requests of neighbouring lanes fill whole lines (with 32 bytes a thread in a row 102 us for 97, then); what
+// follows from a lane's place is computed in the loops, or it is spilled ahead of them, 100 MB of stores (97 for 82).
+// 12 drafts or 128 single tokens: 6 us, a chain of length, page, exponent and codes.
 #include "q8_kv_append.hpp"
 
 namespace q8 {
@@ -156,8 +157,8 @@ __device__ __forceinline__ float item_max(float v, float* red) {
   return v;
 }
 
-// A lane's place, so that what follows from it is computed in the loop (over pages, of which there is one as a
-// rule) and not kept in registers ahead of it
+// A lane's place, so that what follows from it is computed in the loop (which most threads run once) and not
+// kept in registers ahead of it
 __device__ __forceinline__ int in_loop(int place) {
   asm volatile("" : "+v"(place));
   return place;
@@ -454,13 +455,16 @@ __device__ __forceinline__ void norm_queries(const AppendArgs& a, int s, int blo
   const int len = kv.kv_len[s], past = (len < 0 ? 0 : len) - (end - first);
   const int spans = (a.heads + span - 1) / span, per = U * spans;
   const int64_t all = (int64_t)(end - first) * per;
-  const int u = threadIdx.x % U;                             // (blocks of threads are whole heads)
-  const Groups g = groups_of<D>(a, u);
   float w0[8], w1[8];
-  load_weight(a, a.qw, g.c0, w0);
-  load_weight(a, a.qw, g.c1, w1);
+  {
+    const Groups g = groups_of<D>(a, threadIdx.x % U);       // (blocks of threads are whole heads)
+    load_weight(a, a.qw, g.c0, w0);
+    load_weight(a, a.qw, g.c1, w1);
+  }
   for (int64_t i = (int64_t)block * threads + threadIdx.x; i < all; i += (int64_t)blocks * threads) {
     const int t = (int)(i / per), h0 = (int)(i - (int64_t)t * per) / U * span;
+    const int u = in_loop(threadIdx.x) % U;
+    const Groups g = groups_of<D>(a, u);
     float co[8], si[8];
     if (a.rot) load_angles(a, g, u, turned_by(a, first + t, past + t), co, si);
     const int64_t from = (int64_t)(first + t) * a.q_stride, to = (int64_t)(first + t) * a.heads * D;
