@@ -37,7 +37,7 @@ def layers(*pointers):
 
 def compact(n=2, **kw):
     a = dict(k=layers(A, A + 4096), ke=layers(A, A), v=layers(A, A), ve=layers(A, A), layers=n, Hkv=4, D=128, start=A,
-             len=A + 512, table=A + 1024, S=2, mp=10, np=50, page=64, keep=A + 2048, width=5, kept=A + 3072, out=A + 4096,
+             len=A + 512, table=A + 1024, S=2, mp=10, np=50, page=64, keep=A + 2048, width=5, kept=A + 2560, out=A + 4096,
              st=None)
     a.update(kw)
     return E.lib().q8_kv_compact(*a.values())
