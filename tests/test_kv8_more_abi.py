@@ -105,7 +105,7 @@ def test_layers_arguments():
         assert call(len=A + 2) == 6
     assert compact(start=None) == 1 and compact(keep=None) == 1 and compact(kept=None) == 1 and compact(out=None) == 1
     assert compact(width=-1) == 2 and compact(keep=A + 2050) == 6 and compact(out=A + 4098) == 6
-    for same in (A, A + 8, A + 508, A + 512, A + 1024 + 76, A + 2048 + 36, A + 3076):      # the outputs over an input
+    for same in (A, A + 8, A + 508, A + 512, A + 1024 + 76, A + 2048 + 36, A + 2564):      # the outputs over an input
         assert compact(out=same) == 5, hex(same)
 
 
