@@ -137,9 +137,11 @@ struct TreeRows {
             fix = __builtin_amdgcn_exp2f(m[r] - ref + (e[r] - to));
             e[r] = to;
             gap[r] = seen ? own_b - e[r] : 0.0f;
-            share[r] = 0.0f;
-            l[r] += sum;
-            if constexpr (LW) l16[r] += sum;
+            // (where the rounded weights count, those of pages not far below go on as they are below)
+            const bool near = LW && gap[r] >= -kTreeGap;
+            share[r] = near ? __builtin_amdgcn_exp2f(-(gap[r] + kTreeUp)) : 0.0f;
+            l[r] += near ? 0.0f : sum;
+            if constexpr (LW) l16[r] += near ? 0.0f : sum;
           }
         }
         m[r] = mn;

@@ -80,9 +80,11 @@ __device__ __forceinline__ int drafted_at(const AttnArgs& a, int first, int tok,
 }
 
 // The sum that divides an output of f16: of the weights as they are rounded for the product, so that the
-// rounding of a weight that is most of its row's sum cancels (an f16 output of a few keys 1.7e-4 off instead
-// of 2.8e-4, its own rounding being 1.5e-4; a bf16 output's rounding hides it).  The log-sum-exp has the sum
-// of the weights as they are.
+// rounding of a weight that is most of its row's sum cancels (f16 outputs 2.1e-4 to 2.2e-4 off in the root mean
+// square instead of 2.9e-4, their own rounding being 2.0e-4; a bf16 output's rounding hides it, 1.62e-3 against
+// 1.61e-3).  Keys of a page whose value exponent lies more than the gap below the row's have their weights as
+// they are in it: of such a weight little or nothing is left in f16, and all of it in the sum.  The log-sum-exp
+// has the sum of the weights as they are.
 template <int DT, bool TREE>
 inline constexpr bool kOfRounded = TREE && DT == DT_F16;
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
@@ -463,13 +465,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_tiles(const 
           fix = __builtin_amdgcn_exp2f(m - ref + (e - to));
           e = to;
           gap = seen ? vb - e : 0.0f;
-          share = 0.0f;
+          // (where the rounded weights count, those of pages not far below go on as they are below)
+          const bool near = LW && gap >= -kGap;
+          share = near ? __builtin_amdgcn_exp2f(-(gap + kUp)) : 0.0f;
           if (!again) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sn[t][r], kscale, -ref));
+                float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sn[t][r], kscale, -ref));
+                if constexpr (LW) p = near ? 0.0f : p;
                 l += p;
                 if constexpr (LW) lr16 += p;
                 asm volatile("" : "+v"(l));        // one after the other: the registers are all taken
