@@ -865,19 +865,48 @@ q8_status q8_attention_kv8_tree(const void* q, int64_t q_stride, q8_dtype dtype,
 
 namespace {
 
-// The caches of all layers: every pointer given and aligned, no layer twice.
+// The caches of all layers: every pointer given and aligned.
 q8_status check_layers(uint8_t* const* k, uint8_t* const* ke, uint8_t* const* v, uint8_t* const* ve, int64_t layers) {
   if (layers < 1 || layers > kMaxLayers) return Q8_ERR_BAD_SHAPE;
   if (!k || !ke || !v || !ve) return Q8_ERR_NULL_PTR;
-  uintptr_t seen[kMaxLayers];
   for (int64_t i = 0; i < layers; ++i) {
     if (!k[i] || !ke[i] || !v[i] || !ve[i]) return Q8_ERR_NULL_PTR;
     if (!aligned16(k[i]) || !aligned16(v[i])) return Q8_ERR_ALIGN;
-    seen[i] = reinterpret_cast<uintptr_t>(k[i]);
   }
-  std::sort(seen, seen + layers);
-  return std::adjacent_find(seen, seen + layers) == seen + layers ? Q8_OK : Q8_ERR_BAD_ARG;
+  return Q8_OK;
 }
+// The memory of a call over the caches: no array that is written may share any with another.
+struct Ranges {
+  struct Range {
+    uintptr_t from, to;
+    bool written;
+  } r[4 * kMaxLayers + 16];
+  int n = 0;
+  void add(const void* p, int64_t bytes, bool written) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (bytes > 0) r[n++] = Range{at, at + (uint64_t)bytes, written};
+  }
+  void ints(const void* p, int64_t count, bool written) { add(p, 4 * count, written); }
+  void caches(uint8_t* const* k, uint8_t* const* ke, uint8_t* const* v, uint8_t* const* ve, int64_t layers, int64_t pages,
+              int64_t Hkv, int64_t page, int64_t D) {
+    for (int64_t i = 0; i < layers; ++i) {
+      add(k[i], pages * Hkv * page * D, true);
+      add(v[i], pages * Hkv * page * D, true);
+      add(ke[i], pages * Hkv, true);
+      add(ve[i], pages * Hkv, true);
+    }
+  }
+  bool apart() {
+    std::sort(r, r + n, [](const Range& a, const Range& b) { return a.from < b.from; });
+    uintptr_t read = 0, written = 0;               // the ends of what lies before
+    for (int i = 0; i < n; ++i) {
+      if (r[i].from < written || (r[i].written && r[i].from < read)) return false;
+      uintptr_t& end = r[i].written ? written : read;
+      end = end > r[i].to ? end : r[i].to;
+    }
+    return true;
+  }
+};
 q8_status check_layer_ptrs(hipStream_t st, uint8_t* const* k, uint8_t* const* ke, uint8_t* const* v, uint8_t* const* ve,
                            int64_t layers) {
   for (int64_t i = 0; i < layers; ++i) Q8_TRY(check_ptrs(st, {k[i], ke[i], v[i], ve[i]}));
@@ -887,11 +916,6 @@ void take_layers(q8::CacheLayer* to, uint8_t* const* k, uint8_t* const* ke, uint
                  int64_t from, int n) {
   for (int i = 0; i < n; ++i) to[i] = q8::CacheLayer{k[from + i], v[from + i], ke[from + i], ve[from + i]};
 }
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {       // of int32 arrays
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + 4 * (uint64_t)nb && y < x + 4 * (uint64_t)na;
-}
-
 struct ForkWs { size_t first, fresh, taken, copies, total; };
 ForkWs fork_ws(int64_t S, int64_t S_out, int64_t num_pages) {
   Carve c;
@@ -917,10 +941,15 @@ q8_status q8_kv_compact(uint8_t* const* k_cache, uint8_t* const* k_exp, uint8_t*
   if (!aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) || !aligned4(keep) || !aligned4(n_keep) ||
       !aligned4(len_out))
     return Q8_ERR_ALIGN;
-  // every workgroup reads these while one of them writes the lengths
-  if (overlap(len_out, S, kv_len, S) || overlap(len_out, S, q_start, S + 1) || overlap(len_out, S, n_keep, S) ||
-      overlap(len_out, S, block_table, S * max_pages) || (keep && overlap(len_out, S, keep, S * max_keep)))
-    return Q8_ERR_BAD_ARG;
+  Ranges mem;
+  mem.caches(k_cache, k_exp, v_cache, v_exp, layers, num_pages, Hkv, page, D);
+  mem.ints(len_out, S, true);                      // (every workgroup reads the others while one writes it)
+  mem.ints(kv_len, S, false);
+  mem.ints(q_start, S + 1, false);
+  mem.ints(n_keep, S, false);
+  mem.ints(block_table, S * max_pages, false);
+  mem.ints(keep, S * max_keep, false);
+  if (!mem.apart()) return Q8_ERR_BAD_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   Q8_TRY(check_device(st));
   Q8_TRY(check_ptrs(st, {q_start, kv_len, block_table, keep, n_keep, len_out}));
@@ -960,20 +989,18 @@ q8_status q8_kv_fork(uint8_t* const* k_cache, uint8_t* const* k_exp, uint8_t* co
   if (!aligned4(block_table) || !aligned4(kv_len) || !aligned4(refs) || !aligned4(parent) || !aligned4(table_out) ||
       !aligned4(len_out) || !aligned4(refs_out) || !aligned4(missing) || !aligned16(workspace))
     return Q8_ERR_ALIGN;
-  // nothing is written over what is read, or twice
-  struct Array {
-    const void* p;
-    int64_t n;
-  };
-  const Array out[] = {{table_out, S_out * max_pages}, {len_out, S_out}, {refs_out, num_pages}, {missing, 1},
-                       {workspace, (int64_t)(ws.total / 4)}};
-  const Array in[] = {{block_table, S * max_pages}, {kv_len, S}, {refs, num_pages}, {parent, S_out}};
-  for (const Array& o : out) {
-    for (const Array& i : in)
-      if (overlap(o.p, o.n, i.p, i.n)) return Q8_ERR_BAD_ARG;
-    for (const Array& other : out)
-      if (&other != &o && overlap(o.p, o.n, other.p, other.n)) return Q8_ERR_BAD_ARG;
-  }
+  Ranges mem;
+  mem.caches(k_cache, k_exp, v_cache, v_exp, layers, num_pages, Hkv, page, D);
+  mem.ints(table_out, S_out * max_pages, true);
+  mem.ints(len_out, S_out, true);
+  mem.ints(refs_out, num_pages, true);
+  mem.ints(missing, 1, true);
+  mem.add(workspace, (int64_t)ws.total, true);
+  mem.ints(block_table, S * max_pages, false);
+  mem.ints(kv_len, S, false);
+  mem.ints(refs, num_pages, false);
+  mem.ints(parent, S_out, false);
+  if (!mem.apart()) return Q8_ERR_BAD_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   Q8_TRY(check_device(st));
   Q8_TRY(check_ptrs(st, {block_table, kv_len, refs, parent, table_out, len_out, refs_out, missing, workspace}));
