@@ -29,14 +29,14 @@ __device__ __forceinline__ double dpp_f64(double v) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xF, 0xF, false);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// over N neighbouring lanes (4 to 32), which all run this together
+// over N neighbouring lanes (4, 8 or 16), which all run this together
 template <int N>
 __device__ __forceinline__ double lanes_sum(double v) {
+  static_assert(N == 4 || N == 8 || N == 16, "lanes of a head");
   v += dpp_f64<0xB1>(v);
   v += dpp_f64<0x4E>(v);
   if constexpr (N >= 8) v += dpp_f64<0x141>(v);
   if constexpr (N >= 16) v += dpp_f64<0x140>(v);
-  if constexpr (N >= 32) v += __shfl_xor(v, 16);
   return v;
 }
 __device__ __forceinline__ double squares8(const float* v, double sum) {
