@@ -511,8 +511,8 @@ size_t q8_attention_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int
  * go to p + i by the append's rule, their values being what their codes stand
  * for: each (page, kv head, tensor) that receives tokens:
  *     want = least b >= 0 with max |moved values| <= 448 2^(b - 127)
- *     b'   = want if the page's first slot receives one, else max(b, want)
- *     slots before the first that receives one: codes c -> e4m3_rne(e4m3(c) 2^(b - b'))
+ *     b'   = want if the page's first slot is one of the p + i, else max(b, want)
+ *     slots before the first of the p + i in the page: codes c -> e4m3_rne(e4m3(c) 2^(b - b'))
  *     a token from a page of byte u: code c -> e4m3_rne(e4m3(c) 2^(u - b')); NaN codes stay as they are
  * Other slots keep their bytes (those behind the kept tokens are no longer
  * read).  len_out[s] = p + the number kept.
