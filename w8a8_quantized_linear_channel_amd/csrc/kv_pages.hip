@@ -16,6 +16,10 @@
 // ones, numbered by row and entry; then any number of workgroups copy pages.
 // The tables take 5 to 6 us, a chain of passes over LDS between barriers of one workgroup (33 us with counts in
 // device memory and the device's fences); 12 layers' open pages of 64 beams, 63 MB read and written, 11 us behind them.
+// That holds for tables of up to a thousand entries.  The workgroup goes through all sequences' entries three times,
+// 1024 at once: 32 sequences of 128 entries take 11 us, of 512 25, 128 of 512 (a tenth of them filled) 41.  Past 16384
+// pages or 1024 rows the counts are in device memory, some 5 times as slow: 64 sequences of 512 entries on 29576
+// pages 130 us, 128 on 59144 256 (kernel trace).
 #include "q8_device.hpp"
 #include "q8_kv.hpp"
 

@@ -183,7 +183,8 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, const Span& sp, int p
 //
 // The running maximum is a reference that is only moved when a score passes it
 // by 8 (p up to 2^8 costs no precision): most steps neither rescale nor exchange
-// anything between lanes.
+// anything between lanes.  It moves for all rows of a wave at once, and so do
+// their exponents: how a row's weights round can depend on its neighbours' scores.
 //
 // Bound by the matrix units at the clock that the power leaves them: the prompt
 // of 8192 tokens is 550 G flop in 572 us once the clock has settled, 0.96

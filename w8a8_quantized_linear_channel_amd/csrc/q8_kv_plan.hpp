@@ -96,6 +96,7 @@ inline AttnPlan tree_plan(int64_t rows, int dim, int kv_heads, int seqs, int64_t
   // features, shared against 16 or 32 rows a workgroup: 240 rows on 60000 keys 85 against 111 us, 600 on 20000 85
   // against 129, 2 sequences of 160 on up to 60000 136 against 155, 240 on 8000 35 against 29), or very much (32
   // sequences of 256 rows on 4000 125 against 157, of 176 rows 109 against 102; 4 of 732 on 4000 99 against 60).
+  // (Between three fifths and three quarters full only the 160 rows of 256 were timed on such keys.)
   // Sequences and heads that alone pass a launch of that kernel: the other's grid has them in y and z.
   const int64_t most = dim == 256 ? 128 : 256, whole = (rows + most - 1) / most * most;
   const double work = (double)pairs * (double)rows * (double)keys * dim;
@@ -112,7 +113,8 @@ inline AttnPlan tree_plan(int64_t rows, int dim, int kv_heads, int seqs, int64_t
   // Splits only to give every CU a workgroup (32 sequences of 32 rows on 4000 keys: none 39 us, as many as
   // make 512 workgroups 45, 1024 53), but none longer than 8192 keys with few rows, so that one long sequence
   // among many does not hold up the rest.  A share under 1024 keys costs the join more than it saves (one
-  // sequence of 48 rows on 700 keys 11.2 us whole, 13.2 in two), of 256 features under 512.
+  // sequence of 48 rows on 700 keys 11.2 us whole, 13.2 in two), of 256 features under 512.  All sequences have
+  // the shares of the longest: of the 256 workgroups of sequences of 23662 and 59864 keys 72 have none.
   int64_t want = 256 / groups;
   const int64_t least = many ? 256 : dim == 256 ? 512 : 1024;
   if (!many && want < keys / 8192) want = keys / 8192;
