@@ -499,8 +499,8 @@ size_t q8_attention_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int
 /*
  * Calls over the caches of all layers, which share one block table: k_cache,
  * k_exp, v_cache and v_exp are arrays in HOST memory of `layers` device pointers
- * (1 to 512, read before the call returns).  No two of these caches' arrays, and
- * none of them and of the call's other arrays, overlap (Q8_ERR_BAD_ARG).
+ * (1 to 512, read before the call returns).  None of the caches' arrays overlaps
+ * another one or any other array of the call (Q8_ERR_BAD_ARG).
  *
  * q8_kv_compact -- the drafts of a batch that are kept go to the front of their
  * slots, in place.  keep[s, i], i < n_keep[s]: the new token (0 .. n-1, as
